@@ -18,6 +18,7 @@ import torch
 
 __all__ = ["fwd", "fwd_halo", "fwd_fp8", "bwd", "bwd_edges", "bwd_halo", "bwd_noalloc", "bwd_workspace_size", "decode_step", "prefill_to_ring", "prefill_to_ring_varlen",
            "global_fwd", "global_decode_step", "global_decode_workspace_size",
+           "sink_fwd", "sink_decode_step", "prefill_to_sinks",
            "get_last_device_error", "SwaError", "Params", "lib", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libswa.so")
@@ -84,6 +85,12 @@ def lib():
         L.swa_global_decode_step.argtypes = [P] + [_vp] * 8 + [ctypes.c_int64, _vp, _vp,
                                                                ctypes.c_size_t, _vp]
         L.swa_global_decode_step.restype = ctypes.c_int
+        L.swa_sink_fwd.argtypes = [P, ctypes.c_int32] + [_vp] * 9
+        L.swa_sink_fwd.restype = ctypes.c_int
+        L.swa_sink_decode_step.argtypes = [P, ctypes.c_int32] + [_vp] * 13
+        L.swa_sink_decode_step.restype = ctypes.c_int
+        L.swa_prefill_to_sinks.argtypes = [P, ctypes.c_int32] + [_vp] * 9
+        L.swa_prefill_to_sinks.restype = ctypes.c_int
         L.swa_error_string.argtypes = [ctypes.c_int]
         L.swa_error_string.restype = ctypes.c_char_p
         L.swa_get_last_device_error.argtypes = [_vp, ctypes.POINTER(ctypes.c_int)]
@@ -474,6 +481,78 @@ def prefill_to_ring_varlen(k, v, wk, k_cache, v_cache, starts, lens, pos0=None, 
                                           _ptr(k), _ptr(v), _ptr(wk), _ptr(k_cache),
                                           _ptr(v_cache), _stream(stream))
     _check(rc, "swa_prefill_to_ring_varlen")
+
+
+def sink_fwd(q, k, v, g, wq, wk, n_sink, *, window=128, rot_dim=42, rope_base=1e4, eps=1e-6,
+             scale=0.0, out=None, lse=None, want_lse=False, flags=0, stream=None):
+    """:func:`fwd` with the first ``n_sink`` tokens of every sequence visible to all
+    later ones (swa_sink_fwd)."""
+    B, T, Hq, D = q.shape
+    Hkv = k.shape[2]
+    if out is None:
+        out = torch.empty_like(q)
+    if want_lse and lse is None:
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
+    p = make_params(B, T, Hq, Hkv, head_dim=D, window=window, rot_dim=rot_dim,
+                    rope_base=rope_base, eps=eps, scale=scale, flags=flags)
+    nq, nk = B * T * Hq * D, B * T * Hkv * D
+    bf, f32 = torch.bfloat16, torch.float32
+    opt = {} if lse is None else {"lse": (lse, f32, B * Hq * T)}
+    _need("swa_sink_fwd", q.device, q=(q, bf, nq), k=(k, bf, nk), v=(v, bf, nk), g=(g, bf, nq),
+          wq=(wq, f32, D if nq else 0), wk=(wk, f32, D if nq else 0), out=(out, bf, nq), **opt)
+    rc = lib().swa_sink_fwd(ctypes.byref(p), n_sink, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(wq),
+                            _ptr(wk), _ptr(out), _ptr(lse), _stream(stream))
+    _check(rc, "swa_sink_fwd")
+    return (out, lse) if lse is not None else out
+
+
+def sink_decode_step(pos, q, k_new, v_new, g, wq, wk, k_cache, v_cache, k_sink, v_sink, *,
+                     rot_dim=42, rope_base=1e7, eps=1e-6, scale=0.0, out=None, flags=0,
+                     stream=None):
+    """:func:`decode_step` with sinks (swa_sink_decode_step): k_sink, v_sink
+    [N,Hkv,n_sink,128] bf16 hold k', v of positions 0 .. n_sink-1 and are updated
+    in place, as are the rings; returns o [N,Hq,128]."""
+    N, Hq, D = q.shape
+    Hkv, W, S = k_cache.shape[1], k_cache.shape[2], k_sink.shape[2]
+    if out is None:
+        out = torch.empty_like(q)
+    p = make_params(N, 1, Hq, Hkv, head_dim=D, window=W, rot_dim=rot_dim, rope_base=rope_base,
+                    eps=eps, scale=scale, flags=flags)
+    nq, nk = N * Hq * D, N * Hkv * D
+    bf, f32 = torch.bfloat16, torch.float32
+    _need("swa_sink_decode_step", q.device, pos=(pos, torch.int64, N), q=(q, bf, nq),
+          k_new=(k_new, bf, nk), v_new=(v_new, bf, nk), g=(g, bf, nq),
+          wq=(wq, f32, D if N else 0), wk=(wk, f32, D if N else 0),
+          k_cache=(k_cache, bf, nk * W), v_cache=(v_cache, bf, nk * W),
+          k_sink=(k_sink, bf, nk * S), v_sink=(v_sink, bf, nk * S), out=(out, bf, nq))
+    rc = lib().swa_sink_decode_step(ctypes.byref(p), S, _ptr(pos), _ptr(q), _ptr(k_new),
+                                    _ptr(v_new), _ptr(g), _ptr(wq), _ptr(wk), _ptr(k_cache),
+                                    _ptr(v_cache), _ptr(k_sink), _ptr(v_sink), _ptr(out),
+                                    _stream(stream))
+    _check(rc, "swa_sink_decode_step")
+    return out
+
+
+def prefill_to_sinks(k, v, wk, k_sink, v_sink, starts=None, lens=None, pos0=None, *, Hq,
+                     rot_dim=42, rope_base=1e7, eps=1e-6, stream=None):
+    """Fill the [B,Hkv,n_sink,128] sink caches after a prefill (swa_prefill_to_sinks):
+    k, v [B,T,Hkv,128], or with starts and lens (and pos0) rows [T,Hkv,128] as in
+    :func:`prefill_to_ring_varlen`."""
+    B, Hkv, S, D = k_sink.shape
+    T = k.shape[1] if lens is None else k.shape[0]
+    p = make_params(B, T, Hq, Hkv, head_dim=D, rot_dim=rot_dim, rope_base=rope_base, eps=eps)
+    i64, bf = torch.int64, torch.bfloat16
+    n = B * Hkv * S * D
+    nk = (B if lens is None else 1) * T * Hkv * D if n else 0
+    extra = {name: (t, i64, B) for name, t in (("starts", starts), ("lens", lens), ("pos0", pos0))
+             if t is not None}
+    _need("swa_prefill_to_sinks", k_sink.device, k=(k, bf, nk), v=(v, bf, nk),
+          wk=(wk, torch.float32, D if n else 0), k_sink=(k_sink, bf, n), v_sink=(v_sink, bf, n),
+          **extra)
+    rc = lib().swa_prefill_to_sinks(ctypes.byref(p), S, _ptr(starts), _ptr(lens), _ptr(pos0),
+                                    _ptr(k), _ptr(v), _ptr(wk), _ptr(k_sink), _ptr(v_sink),
+                                    _stream(stream))
+    _check(rc, "swa_prefill_to_sinks")
 
 
 def get_last_device_error(stream=None):

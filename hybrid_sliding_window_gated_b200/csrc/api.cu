@@ -10,6 +10,7 @@
 #include "bwd_internal.h"
 #include "decode_internal.h"
 #include "global_internal.h"
+#include "sink_internal.h"
 #include "swa_internal.h"
 
 namespace swa {
@@ -690,6 +691,157 @@ int swa_global_decode_step(const swa_params_t* p, const int64_t* pos, const swa_
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if ((rc = launch_global_kv(kv, p->B, st)) != SWA_OK) return rc;
   return launch_global_decode(tk, tv, a, st);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- sink tokens
+
+namespace swa {
+
+// Shape checks of the sink entry points: the window layers' own, and n_sink.
+static int check_params_sink(const swa_params_t* p, int32_t n_sink, bool decode) {
+  const int rc = check_params(p, decode);
+  if (rc == SWA_ERR_INVALID_ARG) return rc;
+  if (n_sink < 0) return SWA_ERR_INVALID_ARG;
+  if (rc != SWA_OK) return rc;
+  return n_sink > kMaxSink ? SWA_ERR_UNSUPPORTED : SWA_OK;
+}
+
+}  // namespace swa
+
+extern "C" {
+
+int swa_sink_fwd(const swa_params_t* p, int32_t n_sink, const swa_bf16_t* q, const swa_bf16_t* k,
+                 const swa_bf16_t* v, const swa_bf16_t* g, const float* wq, const float* wk,
+                 swa_bf16_t* o, float* lse, void* stream) {
+  int rc = check_params_sink(p, n_sink, false);
+  if (rc != SWA_OK) return rc;
+  if (p->B == 0 || p->T == 0) return SWA_OK;
+  if (!q || !k || !v || !g || !wq || !wk || !o) return SWA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(g) || !aligned16(o) ||
+      !aligned16(wq) || !aligned16(wk) || (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return SWA_ERR_INVALID_ARG;
+  SinkFwdArgs a{};
+  a.B = static_cast<int>(p->B);
+  a.T = static_cast<int>(p->T);
+  a.Hq = p->Hq;
+  a.Hkv = p->Hkv;
+  a.G = p->Hq / p->Hkv;
+  a.n_sink = n_sink;
+  a.half_rot = p->rot_dim / 2;
+  a.tiles = static_cast<int>((p->T + kSinkTile - 1) / kSinkTile);
+  if (p->B * p->Hkv > 0x7fffffffll) return SWA_ERR_UNSUPPORTED;  // chains are counted in 32 bits
+  a.total_tiles = static_cast<long long>(a.tiles) * p->B * p->Hkv;
+  if (a.total_tiles > (1ll << 24)) return SWA_ERR_UNSUPPORTED;  // a CTA's jobs are counted in 32 bits
+  a.scale_log2 = score_scale(p) * 1.4426950408889634f;
+  a.eps = p->eps;
+  a.flags = p->flags;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.g = g;
+  a.wq = wq;
+  a.wk = wk;
+  a.o = o;
+  a.lse = lse;
+  if ((rc = device_error_word(&a.err)) != SWA_OK) return rc;
+  fill_inv_freq(p, a.inv_freq);
+  return launch_sink_fwd(a, static_cast<cudaStream_t>(stream));
+}
+
+int swa_sink_decode_step(const swa_params_t* p, int32_t n_sink, const int64_t* pos,
+                         const swa_bf16_t* q, const swa_bf16_t* k_new, const swa_bf16_t* v_new,
+                         const swa_bf16_t* g, const float* wq, const float* wk,
+                         swa_bf16_t* k_cache, swa_bf16_t* v_cache, swa_bf16_t* k_sink,
+                         swa_bf16_t* v_sink, swa_bf16_t* o, void* stream) {
+  int rc = check_params_sink(p, n_sink, true);
+  if (rc != SWA_OK) return rc;
+  if (p->Hq / p->Hkv > kDecMaxGroup) return SWA_ERR_UNSUPPORTED;
+  if (p->B == 0) return SWA_OK;
+  if (!pos || !q || !k_new || !v_new || !g || !wq || !wk || !k_cache || !v_cache || !o ||
+      (n_sink > 0 && (!k_sink || !v_sink)))
+    return SWA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(pos) & 7u) || !aligned16(q) || !aligned16(k_new) ||
+      !aligned16(v_new) || !aligned16(g) || !aligned16(wq) || !aligned16(wk) ||
+      !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) ||
+      (n_sink > 0 && (!aligned16(k_sink) || !aligned16(v_sink))))
+    return SWA_ERR_INVALID_ARG;
+  SinkDecArgs a{};
+  a.N = static_cast<int>(p->B);
+  a.Hq = p->Hq;
+  a.Hkv = p->Hkv;
+  a.G = p->Hq / p->Hkv;
+  a.n_sink = n_sink;
+  a.s8 = (n_sink + 7) / 8 * 8;
+  a.half_rot = p->rot_dim / 2;
+  a.flags = p->flags;
+  a.scale_log2 = score_scale(p) * 1.4426950408889634f;
+  a.eps = p->eps;
+  a.pos = pos;
+  a.q = q;
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.g = g;
+  a.wq = wq;
+  a.wk = wk;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_sink = k_sink;
+  a.v_sink = v_sink;
+  a.o = o;
+  if ((rc = device_error_word(&a.err)) != SWA_OK) return rc;
+  fill_inv_freq(p, a.inv_freq);
+  CUtensorMap tk, tv;
+  const uint64_t D = kHeadDim, W = kWindow, N = p->B;
+  if ((rc = encode_tmap_4d(&tk, k_cache, D, W, p->Hkv, N, 64, kWindow, 1, 1,
+                           CU_TENSOR_MAP_SWIZZLE_128B)) ||
+      (rc = encode_tmap_4d(&tv, v_cache, D, W, p->Hkv, N, 64, kWindow, 1, 1,
+                           CU_TENSOR_MAP_SWIZZLE_128B)))
+    return rc;
+  // The sinks in boxes of 8 or 16 rows: rows past n_sink arrive as zeros.
+  CUtensorMap tks = tk, tvs = tv;
+  if (n_sink > 0 &&
+      ((rc = encode_tmap_4d(&tks, k_sink, D, n_sink, p->Hkv, N, 64, a.s8, 1, 1,
+                            CU_TENSOR_MAP_SWIZZLE_128B)) ||
+       (rc = encode_tmap_4d(&tvs, v_sink, D, n_sink, p->Hkv, N, 64, a.s8, 1, 1,
+                            CU_TENSOR_MAP_SWIZZLE_128B))))
+    return rc;
+  return launch_sink_decode(tk, tv, tks, tvs, a, static_cast<cudaStream_t>(stream));
+}
+
+int swa_prefill_to_sinks(const swa_params_t* p, int32_t n_sink, const int64_t* starts,
+                         const int64_t* lens, const int64_t* pos0, const swa_bf16_t* k,
+                         const swa_bf16_t* v, const float* wk, swa_bf16_t* k_sink,
+                         swa_bf16_t* v_sink, void* stream) {
+  int rc = check_params_sink(p, n_sink, false);
+  if (rc != SWA_OK) return rc;
+  if ((starts == nullptr) != (lens == nullptr) || (pos0 != nullptr && lens == nullptr))
+    return SWA_ERR_INVALID_ARG;
+  if (p->B == 0 || n_sink == 0 || (p->T == 0 && lens == nullptr)) return SWA_OK;
+  if (!wk || !k_sink || !v_sink || (p->T > 0 && (!k || !v))) return SWA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(starts) & 7u) || (reinterpret_cast<uintptr_t>(lens) & 7u) ||
+      (reinterpret_cast<uintptr_t>(pos0) & 7u) || !aligned16(k) || !aligned16(v) ||
+      !aligned16(wk) || !aligned16(k_sink) || !aligned16(v_sink))
+    return SWA_ERR_INVALID_ARG;
+  SinkFillArgs a{};
+  a.B = static_cast<int>(p->B);
+  a.T = static_cast<int>(p->T);
+  a.Hkv = p->Hkv;
+  a.n_sink = n_sink;
+  a.half_rot = p->rot_dim / 2;
+  a.eps = p->eps;
+  a.k = k;
+  a.v = v;
+  a.wk = wk;
+  a.k_sink = k_sink;
+  a.v_sink = v_sink;
+  a.starts = starts;
+  a.lens = lens;
+  a.pos0 = pos0;
+  if ((rc = device_error_word(&a.err)) != SWA_OK) return rc;
+  fill_inv_freq(p, a.inv_freq);
+  return launch_sink_fill(a, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,501 @@
+// sink_decode.cu -- one decode step of the gated sliding-window attention with
+// sink tokens, and the prefill -> sink cache handoff, for sm_100a.
+//
+// A sequence keeps a 128-slot ring of its last tokens and a cache of its first
+// n_sink tokens' k' and v.  The new token at position p attends over the ring
+// (slot s holds position p - ((p - s) mod W), ignored when negative) and over
+// the sinks s <= p - W, which have left the ring.  A token with p < n_sink is a
+// sink itself and is written to both.
+//
+// What bounds it: memory.  A unit is one (sequence, KV head): 64 KiB of ring,
+// 512 bytes per sink and 2.5 KiB of new rows.  As in the plain decode step a
+// persistent CTA streams its units: a producer warp keeps the next ones in
+// flight by TMA (128-byte swizzle) and two groups of four warps take alternate
+// units, warp w of a group slots 32 w .. 32 w + 31; one of the warps also takes
+// the sinks, as one more 8- or 16-key block of its own softmax, so they cost no
+// further merge.
+//
+// Two bf16 terms at no cost.  The tensor core's A operand has 16 rows and a
+// group at most eight heads, so rows 0-7 carry the bf16 of q' and rows 8-15
+// what that rounding left over, and likewise for P; the two halves of a product
+// are added.  q' and P so enter with 16 bits of mantissa, and only the caches'
+// own bf16 and the output's rounding remain.
+#include <atomic>
+
+#include "decode_internal.h"
+#include "launch.cuh"
+#include "ptx.cuh"
+#include "rowops.cuh"
+#include "sink_internal.h"
+#include "warp_mma.cuh"
+
+namespace swa {
+namespace snd {
+
+constexpr int kGroups = 2;
+constexpr int kThreads = 32 * (1 + 4 * kGroups);
+constexpr int kMaxStages = 3;
+constexpr int kHalf = kWindow * 64 * 2;  // 128 slots x 64 dims (one TMA box)
+constexpr int kQStride = 68;             // words per packed q' row
+constexpr int kOStride = 136;            // floats per partial-O row
+
+struct Group {
+  uint32_t qa[2 * kDecMaxGroup][kQStride];  // q' as bf16 pairs: heads, then their remainders
+  float scratch[4][kHeadDim];
+  float mw[4][kDecMaxGroup], lw[4][kDecMaxGroup];
+};
+struct Control {
+  Group grp[kGroups];
+  uint64_t full[kMaxStages], empty[kMaxStages], never;
+  int abort;
+};
+static_assert(4 * kDecMaxGroup * kOStride * 4 <= 2 * kHalf, "partial O does not fit the K ring");
+
+// A stage: K ring, V ring (two 64-dim halves each), K and V sinks (two halves
+// of s8 rows each), q and g rows, the new k and v, the rotation, the position.
+struct Stage {
+  uint8_t* p;
+  int s8, G;
+  __device__ uint8_t* k() const { return p; }
+  __device__ uint8_t* v() const { return p + 2 * kHalf; }
+  __device__ uint8_t* ks() const { return p + 4 * kHalf; }
+  __device__ uint8_t* vs() const { return p + 4 * kHalf + s8 * 256; }
+  __device__ uint16_t* q() const { return reinterpret_cast<uint16_t*>(p + 4 * kHalf + s8 * 512); }
+  __device__ uint16_t* g() const { return q() + G * kHeadDim; }
+  __device__ uint16_t* kn() const { return g() + G * kHeadDim; }
+  __device__ uint16_t* vn() const { return kn() + kHeadDim; }
+  __device__ float2* rot() const { return reinterpret_cast<float2*>(vn() + kHeadDim); }
+  __device__ long long* pos() const { return reinterpret_cast<long long*>(rot() + kMaxPairs); }
+};
+inline int stage_size(int s8, int G) {
+  const int n = 4 * kHalf + s8 * 512 + 2 * G * kHeadDim * 2 + 2 * kHeadDim * 2 + kMaxPairs * 8 + 8;
+  return (n + 1023) & ~1023;
+}
+
+enum Site { kSiteFull = 0xD0, kSiteEmpty, kSiteForced };
+
+// Byte offset of 16-byte chunk c (0..15) of row s in a [half][row][64] tile with
+// 128-byte swizzle; `half` is the bytes of one half.
+__device__ __forceinline__ uint32_t tile_off(int s, int c, int half) {
+  return static_cast<uint32_t>((c >> 3) * half + s * 128 + (((c & 7) ^ (s & 7)) << 4));
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Barrier over a group's 128 threads that also ANDs v across them.
+__device__ __forceinline__ bool group_and(bool v, int id) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(v)), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
+// bf16 pair of (x, y) and of what the rounding left over.
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16x2(x, y);
+  lo = pack_bf16x2(x - bf16_lo(hi), y - bf16_hi(hi));
+}
+
+__device__ __forceinline__ void process_unit(const Stage& st, Group& gp, const SinkDecArgs& a,
+                                             int n, int kvh, int gi, int lw, int lane) {
+  const int bar_id = 1 + gi;
+  const long long p = *st.pos();
+  if (p < 0) {  // the same value for the whole group
+    if (lw == 0 && lane == 0) atomicCAS(a.err, 0, kDevErrBadPosition);
+    return;
+  }
+  const int s0 = static_cast<int>(p & (kWindow - 1));
+  const int owner = s0 >> 5;
+  const bool sink_warp = a.n_sink > 0 && lw == ((owner + 2) & 3) && p >= kWindow;
+  const int seen = p - kWindow >= a.n_sink ? a.n_sink : static_cast<int>(p - kWindow) + 1;
+
+  float cs = 1.0f, sn = 0.0f;
+  if (lane < a.half_rot) {
+    const float2 r = st.rot()[lane];
+    cs = r.x;
+    sn = r.y;
+  }
+  for (int h = lw; h < a.G; h += 4) {
+    float x[4];
+    load4(st.q() + h * kHeadDim + 4 * lane, x);
+    norm_rope_row(x, a.wq, a.eps, gp.scratch[lw], lane, a.half_rot, cs, sn);
+    uint32_t hi, lo;
+    split2(x[0], x[1], hi, lo);
+    gp.qa[h][2 * lane] = hi;
+    gp.qa[kDecMaxGroup + h][2 * lane] = lo;
+    split2(x[2], x[3], hi, lo);
+    gp.qa[h][2 * lane + 1] = hi;
+    gp.qa[kDecMaxGroup + h][2 * lane + 1] = lo;
+  }
+  // The new token's row into slot s0, in shared memory and in the caches.
+  if (lw == owner) {
+    float x[4];
+    load4(st.kn() + 4 * lane, x);
+    norm_rope_row(x, a.wk, a.eps, gp.scratch[lw], lane, a.half_rot, cs, sn);
+    const uint2 kp = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+    const uint2 vp = *reinterpret_cast<const uint2*>(st.vn() + 4 * lane);
+    const uint32_t off = tile_off(s0, lane >> 1, kHalf) + (lane & 1) * 8;
+    *reinterpret_cast<uint2*>(st.k() + off) = kp;
+    *reinterpret_cast<uint2*>(st.v() + off) = vp;
+    const long long unit = static_cast<long long>(n) * a.Hkv + kvh;
+    const long long row = (unit * kWindow + s0) * kHeadDim + 4 * lane;
+    *reinterpret_cast<uint2*>(a.k_cache + row) = kp;
+    *reinterpret_cast<uint2*>(a.v_cache + row) = vp;
+    if (p < a.n_sink) {
+      const long long srow = (unit * a.n_sink + p) * kHeadDim + 4 * lane;
+      *reinterpret_cast<uint2*>(a.k_sink + srow) = kp;
+      *reinterpret_cast<uint2*>(a.v_sink + srow) = vp;
+    }
+    __syncwarp();
+  }
+  // Slots that hold no token of the sequence may hold anything: their V rows
+  // become zeros, since P = 0 does not hide an infinity or a NaN.
+  {
+    const int s = 32 * lw + lane;
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    bool wrote = false;
+    if (p - ((p - s) & (kWindow - 1)) < 0) {
+#pragma unroll
+      for (int c = 0; c < 16; ++c) *reinterpret_cast<uint4*>(st.v() + tile_off(s, c, kHalf)) = z;
+      wrote = true;
+    }
+    if (sink_warp && lane >= seen && lane < a.s8) {
+#pragma unroll
+      for (int c = 0; c < 16; ++c)
+        *reinterpret_cast<uint4*>(st.vs() + tile_off(lane, c, a.s8 * 128)) = z;
+      wrote = true;
+    }
+    if (wrote) fence_proxy_async_smem();  // before a later copy into this stage
+  }
+  group_and(true, bar_id);  // q', the new row and the zeros are visible to the group
+
+  // ---- S = q' K^T: 4 n-tiles of the ring, 2 of the sinks on one warp
+  const int grp = lane >> 2, tig = lane & 3;
+  const bool row_ok = grp < a.G;
+  float acc[6][4];
+#pragma unroll
+  for (int j = 0; j < 6; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+  const uint32_t kbase = smem_u32(st.k()), ksbase = smem_u32(st.ks());
+#pragma unroll
+  for (int kp2 = 0; kp2 < 4; ++kp2) {
+    uint32_t q0[2], q1[2], q2[2], q3[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int kk = 2 * kp2 + e;
+      q0[e] = row_ok ? gp.qa[grp][8 * kk + tig] : 0u;
+      q1[e] = row_ok ? gp.qa[kDecMaxGroup + grp][8 * kk + tig] : 0u;
+      q2[e] = row_ok ? gp.qa[grp][8 * kk + 4 + tig] : 0u;
+      q3[e] = row_ok ? gp.qa[kDecMaxGroup + grp][8 * kk + 4 + tig] : 0u;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t b[4];
+      ldsm_x4(kbase + tile_off(32 * lw + 8 * j + (lane & 7), 4 * kp2 + (lane >> 3), kHalf), b);
+      mma_16816(acc[j], q0[0], q1[0], q2[0], q3[0], b[0], b[1]);
+      mma_16816(acc[j], q0[1], q1[1], q2[1], q3[1], b[2], b[3]);
+    }
+    if (sink_warp) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (8 * j >= a.s8) break;
+        uint32_t b[4];
+        ldsm_x4(ksbase + tile_off(8 * j + (lane & 7), 4 * kp2 + (lane >> 3), a.s8 * 128), b);
+        mma_16816(acc[4 + j], q0[0], q1[0], q2[0], q3[0], b[0], b[1]);
+        mma_16816(acc[4 + j], q0[1], q1[1], q2[1], q3[1], b[2], b[3]);
+      }
+    }
+  }
+  // ---- softmax of this warp's keys, in log2 units
+  float m = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < 6; ++j)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      bool valid;
+      if (j < 4) {
+        const int s = 32 * lw + 8 * j + 2 * tig + e;
+        valid = p - ((p - s) & (kWindow - 1)) >= 0;
+      } else {
+        valid = sink_warp && 8 * (j - 4) + 2 * tig + e < seen;
+      }
+      acc[j][e] = valid ? (acc[j][e] + acc[j][e + 2]) * a.scale_log2 : -INFINITY;
+      m = fmaxf(m, acc[j][e]);
+    }
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const float mu = m == -INFINITY ? 0.0f : m;
+  float l = 0.0f;
+  uint32_t ph[6], pl[6];
+#pragma unroll
+  for (int j = 0; j < 6; ++j) {
+    const float p0 = ex2_approx(acc[j][0] - mu), p1 = ex2_approx(acc[j][1] - mu);
+    l += p0 + p1;
+    split2(p0, p1, ph[j], pl[j]);
+    if (!row_ok) ph[j] = pl[j] = 0u;
+  }
+  l += __shfl_xor_sync(0xffffffffu, l, 1);
+  l += __shfl_xor_sync(0xffffffffu, l, 2);
+
+  // ---- partial O = P V
+  float oacc[16][4];
+  const uint32_t vbase = smem_u32(st.v()), vsbase = smem_u32(st.vs());
+  // sink keys 8 .. 15 of an 8-row cache have P = 0 and read rows 0 .. 7 again
+  const int srow = a.s8 == 16 ? (lane & 15) : (lane & 7);
+#pragma unroll
+  for (int nd = 0; nd < 16; ++nd) {
+    oacc[nd][0] = oacc[nd][1] = oacc[nd][2] = oacc[nd][3] = 0.0f;
+    uint32_t b[4];
+    ldsm_x4_trans(vbase + tile_off(32 * lw + lane, nd, kHalf), b);
+    mma_16816(oacc[nd], ph[0], pl[0], ph[1], pl[1], b[0], b[1]);
+    mma_16816(oacc[nd], ph[2], pl[2], ph[3], pl[3], b[2], b[3]);
+    if (sink_warp) {
+      ldsm_x4_trans(vsbase + tile_off(srow, nd, a.s8 * 128), b);
+      mma_16816(oacc[nd], ph[4], pl[4], ph[5], pl[5], b[0], b[1]);
+    }
+  }
+  group_and(true, bar_id);  // every warp is done with the K ring: reuse it
+  float* part = reinterpret_cast<float*>(st.k());  // [4][kDecMaxGroup][kOStride]
+  if (row_ok) {
+    float* dst = part + (lw * kDecMaxGroup + grp) * kOStride + 2 * tig;
+#pragma unroll
+    for (int nd = 0; nd < 16; ++nd)
+      *reinterpret_cast<float2*>(dst + 8 * nd) =
+          make_float2(oacc[nd][0] + oacc[nd][2], oacc[nd][1] + oacc[nd][3]);
+    if (tig == 0) {
+      gp.mw[lw][grp] = m;
+      gp.lw[lw][grp] = l;
+    }
+  }
+  fence_proxy_async_smem();  // these writes before a later copy into the stage
+  group_and(true, bar_id);
+
+  // ---- o = (sum_w O_w 2^(m_w - m)) / (sum_w l_w 2^(m_w - m)) * sigmoid(g)
+  for (int h = lw; h < a.G; h += 4) {
+    float mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) mx = fmaxf(mx, gp.mw[w][h]);
+    float f[4], lsum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      f[w] = gp.mw[w][h] == -INFINITY ? 0.0f : ex2_approx(gp.mw[w][h] - mx);
+      lsum += f[w] * gp.lw[w][h];
+    }
+    float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float4 v4 =
+          *reinterpret_cast<const float4*>(part + (w * kDecMaxGroup + h) * kOStride + 4 * lane);
+      y[0] += f[w] * v4.x;
+      y[1] += f[w] * v4.y;
+      y[2] += f[w] * v4.z;
+      y[3] += f[w] * v4.w;
+    }
+    const float inv_l = 1.0f / lsum;
+    float gx[4];
+    load4(st.g() + h * kHeadDim + 4 * lane, gx);
+    float ov[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) ov[e] = y[e] * inv_l / (1.0f + __expf(-gx[e]));
+    *reinterpret_cast<uint2*>(a.o + (static_cast<long long>(n) * a.Hq + kvh * a.G + h) * kHeadDim +
+                              4 * lane) =
+        make_uint2(pack_bf16x2(ov[0], ov[1]), pack_bf16x2(ov[2], ov[3]));
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    sink_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ CUtensorMap tm_ks,
+                       const __grid_constant__ CUtensorMap tm_vs, const SinkDecArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  Control& sm = *reinterpret_cast<Control*>(base + a.stages * a.stage_bytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const long long units = static_cast<long long>(a.N) * a.Hkv;
+  const long long u0 = units * blockIdx.x / gridDim.x;
+  const int n_units = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x - u0);
+
+  if (tid == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      mbar_init(&sm.full[s], 2);  // the copies' expect_tx arrive + the position
+      mbar_init(&sm.empty[s], 1);
+    }
+    mbar_init(&sm.never, 1);
+    sm.abort = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  volatile int* abort = &sm.abort;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      prefetch_tensormap(&tm_k);
+      prefetch_tensormap(&tm_v);
+    }
+    const uint32_t row_bytes = kHeadDim * 2;
+    const uint32_t bytes = 4 * kHalf + a.s8 * 512 + 2 * a.G * row_bytes + 2 * row_bytes;
+    int issued[kMaxStages] = {0};
+    bool ok = true;
+    long long seq = -1, p = 0;
+    float2 rot = make_float2(1.0f, 0.0f);
+    int s = 0, round = 0;
+    for (int i = 0; i < n_units; ++i) {
+      bool w = true;
+      if (lane == 0 && round > 0)
+        w = mbar_wait(&sm.empty[s], (round - 1) & 1, abort, a.err, kSiteEmpty);
+      if (!__shfl_sync(0xffffffffu, w ? 1 : 0, 0)) {
+        ok = false;
+        break;
+      }
+      const long long u = u0 + i;
+      const int n = static_cast<int>(u / a.Hkv), kvh = static_cast<int>(u - u / a.Hkv * a.Hkv);
+      const Stage st{base + s * a.stage_bytes, a.s8, a.G};
+      if (lane == 0) {
+        uint64_t* full = &sm.full[s];
+        mbar_arrive_expect_tx(full, bytes);
+        tma_load_4d(st.k(), &tm_k, full, 0, 0, kvh, n);
+        tma_load_4d(st.k() + kHalf, &tm_k, full, 64, 0, kvh, n);
+        tma_load_4d(st.v(), &tm_v, full, 0, 0, kvh, n);
+        tma_load_4d(st.v() + kHalf, &tm_v, full, 64, 0, kvh, n);
+        if (a.s8 > 0) {
+          tma_load_4d(st.ks(), &tm_ks, full, 0, 0, kvh, n);
+          tma_load_4d(st.ks() + a.s8 * 128, &tm_ks, full, 64, 0, kvh, n);
+          tma_load_4d(st.vs(), &tm_vs, full, 0, 0, kvh, n);
+          tma_load_4d(st.vs() + a.s8 * 128, &tm_vs, full, 64, 0, kvh, n);
+        }
+        const long long qrow = (static_cast<long long>(n) * a.Hq + kvh * a.G) * kHeadDim;
+        const long long kvrow = (static_cast<long long>(n) * a.Hkv + kvh) * kHeadDim;
+        bulk_load(st.q(), a.q + qrow, a.G * row_bytes, full);
+        bulk_load(st.g(), a.g + qrow, a.G * row_bytes, full);
+        bulk_load(st.kn(), a.k_new + kvrow, row_bytes, full);
+        bulk_load(st.vn(), a.v_new + kvrow, row_bytes, full);
+        ++issued[s];
+      }
+      if (n != seq) {
+        seq = n;
+        p = a.pos[n];
+        if (lane < a.half_rot)
+          rope_cos_sin(static_cast<double>(p), a.inv_freq[lane], &rot.x, &rot.y);
+      }
+      if (lane == 0) *st.pos() = p;
+      if (lane < a.half_rot) st.rot()[lane] = rot;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.full[s]);
+      if (++s == a.stages) {
+        s = 0;
+        ++round;
+      }
+    }
+    if (!ok && lane == 0) {
+      for (int i = 0; i < a.stages; ++i)
+        if (issued[i] > 0) mbar_wait_drain(&sm.full[i], (issued[i] - 1) & 1);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------- consumer group
+    const int gi = (warp - 1) >> 2, lw = (warp - 1) & 3;
+    bool live = true;
+    if (a.flags & SWA_FLAG_FORCE_TIMEOUT)
+      live = group_and(mbar_wait(&sm.never, 0, abort, a.err, kSiteForced), 1 + gi);
+    for (int i = gi; live && i < n_units; i += kGroups) {
+      const int s = i % a.stages;
+      const bool got = mbar_wait(&sm.full[s], (i / a.stages) & 1, abort, a.err, kSiteFull);
+      if (!group_and(got, 1 + gi)) break;
+      const long long u = u0 + i;
+      const int n = static_cast<int>(u / a.Hkv), kvh = static_cast<int>(u - u / a.Hkv * a.Hkv);
+      process_unit(Stage{base + s * a.stage_bytes, a.s8, a.G}, sm.grp[gi], a, n, kvh, gi, lw, lane);
+      group_and(true, 1 + gi);
+      if (lw == 0 && lane == 0) mbar_arrive(&sm.empty[s]);
+    }
+  }
+  __syncthreads();
+}
+
+// Prefill -> sink caches: one warp per (sequence, sink) writes k' (rounded as a
+// decode step rounds it) and v of the token at position s, for every KV head;
+// sinks that the sequence's tokens do not reach keep their contents.
+__global__ void __launch_bounds__(128) sink_fill_kernel(const SinkFillArgs a) {
+  __shared__ __align__(16) float scratch[4][kHeadDim];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long gw = static_cast<long long>(blockIdx.x) * 4 + warp;
+  const long long b = gw / a.n_sink;
+  const int s = static_cast<int>(gw - b * a.n_sink);
+  if (b >= a.B) return;
+  long long first = b * a.T, len = a.T, p0 = 0;
+  if (a.lens != nullptr) {
+    first = a.starts[b];
+    len = a.lens[b];
+    p0 = a.pos0 != nullptr ? a.pos0[b] : 0;
+    if (first < 0 || len < 0 || p0 < 0 || len > a.T || first > a.T - len) {
+      if (s == 0 && lane == 0) atomicCAS(a.err, 0, kDevErrBadPosition);
+      return;
+    }
+  }
+  if (s < p0 || s - p0 >= len) return;
+  float cs = 1.0f, sn = 0.0f;
+  if (lane < a.half_rot) rope_cos_sin(static_cast<double>(s), a.inv_freq[lane], &cs, &sn);
+  for (int h = 0; h < a.Hkv; ++h) {
+    const long long row = ((first + (s - p0)) * a.Hkv + h) * kHeadDim;
+    float x[4];
+    load4(a.k + row + 4 * lane, x);
+    const uint2 vv = *reinterpret_cast<const uint2*>(a.v + row + 4 * lane);
+    norm_rope_row(x, a.wk, a.eps, scratch[warp], lane, a.half_rot, cs, sn);
+    const long long dst = ((b * a.Hkv + h) * a.n_sink + s) * kHeadDim + 4 * lane;
+    *reinterpret_cast<uint2*>(a.k_sink + dst) =
+        make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+    *reinterpret_cast<uint2*>(a.v_sink + dst) = vv;
+  }
+}
+
+}  // namespace snd
+
+int launch_sink_decode(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tks,
+                       const CUtensorMap& tvs, SinkDecArgs a, cudaStream_t stream) {
+  DeviceInfo di;
+  int rc = current_device_info(&di);
+  if (rc != SWA_OK) return rc;
+  constexpr int kLimit = 232448;
+  constexpr int kFixed = static_cast<int>(sizeof(snd::Control)) + 1024;
+  a.stage_bytes = snd::stage_size(a.s8, a.G);
+  // Three units in flight where they fit (up to 8 sinks, or 16 with few heads), else two.
+  a.stages = 3 * a.stage_bytes + kFixed <= kLimit ? 3 : 2;
+  static std::atomic<int> configured[64];
+  if (!configured[di.device].load(std::memory_order_acquire)) {
+    cudaError_t e = cudaFuncSetAttribute(snd::sink_decode_kernel,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kLimit);
+    if (e != cudaSuccess) return map_cuda_error(e);
+    configured[di.device].store(1, std::memory_order_release);
+  }
+  const long long units = static_cast<long long>(a.N) * a.Hkv;
+  const long long grid = units < di.num_sms ? units : di.num_sms;
+  return launch_dependent(snd::sink_decode_kernel, static_cast<unsigned>(grid), snd::kThreads,
+                          static_cast<size_t>(a.stages) * a.stage_bytes + kFixed, stream, tk, tv,
+                          tks, tvs, a);
+}
+
+int launch_sink_fill(const SinkFillArgs& a, cudaStream_t stream) {
+  const long long grid = (static_cast<long long>(a.B) * a.n_sink + 3) / 4;
+  if (grid > 0x7fffffffLL) return SWA_ERR_UNSUPPORTED;
+  return launch_dependent(snd::sink_fill_kernel, static_cast<unsigned>(grid), 128, 0, stream, a);
+}
+
+}  // namespace swa

@@ -321,6 +321,53 @@ int swa_global_decode_step(const swa_params_t* p, const int64_t* pos, const swa_
                            int64_t cache_cap, swa_bf16_t* o, void* workspace,
                            size_t workspace_bytes, void* stream);
 
+/*
+ * Sink tokens: the window layers' attention with the first n_sink tokens of
+ * every sequence visible to all later ones.  Query i attends key j when j <= i
+ * and (i - j < window or j < n_sink); a sink inside the window counts once.
+ * Norm, RoPE (at the tokens' own positions), GQA and gate are those of swa_fwd,
+ * and n_sink = 0 is swa_fwd's attention.  0 <= n_sink <= 16 (a negative one
+ * returns SWA_ERR_INVALID_ARG, more than 16 SWA_ERR_UNSUPPORTED).  No
+ * counterpart in the pages: a window layer that streams past its window keeps
+ * the attention mass that the first tokens draw.
+ *
+ * swa_sink_fwd: arguments and results of swa_fwd.  A key that a query does not
+ * see never reaches its output, whatever it holds (NaN and infinities
+ * included), so rows behind a padded sequence may hold anything.
+ */
+int swa_sink_fwd(const swa_params_t* p, int32_t n_sink, const swa_bf16_t* q, const swa_bf16_t* k,
+                 const swa_bf16_t* v, const swa_bf16_t* g, const float* wq, const float* wk,
+                 swa_bf16_t* o, float* lse, void* stream);
+
+/*
+ * One decode step with sinks: swa_decode_step plus the sink caches k_sink,
+ * v_sink [B,Hkv,n_sink,D] bf16 (may be NULL when n_sink is 0), slot s holding
+ * k' and v of position s.  The new token at position pos[n] attends over the
+ * ring and over the sinks s <= pos[n] - window, which have left it; a token with
+ * pos[n] < n_sink is also written to its sink slot.  Slots that hold no token of
+ * the sequence may hold anything.  Other arguments, results and errors as
+ * swa_decode_step.
+ */
+int swa_sink_decode_step(const swa_params_t* p, int32_t n_sink, const int64_t* pos,
+                         const swa_bf16_t* q, const swa_bf16_t* k_new, const swa_bf16_t* v_new,
+                         const swa_bf16_t* g, const float* wq, const float* wk,
+                         swa_bf16_t* k_cache, swa_bf16_t* v_cache, swa_bf16_t* k_sink,
+                         swa_bf16_t* v_sink, swa_bf16_t* o, void* stream);
+
+/*
+ * Prefill -> sink caches (beside swa_prefill_to_ring and its varlen form, which
+ * fill the rings): slot s of k_sink, v_sink [B,Hkv,n_sink,D] receives k' and v of
+ * the token at position s, rounded as swa_sink_decode_step rounds them.  starts
+ * and lens NULL: k, v [B,T,Hkv,D] at positions 0 .. T-1.  Both set: sequence b's
+ * lens[b] tokens are rows starts[b] .. of k, v [p->T,Hkv,D], at positions
+ * pos0[b] .. (pos0 NULL: 0), checked as in swa_prefill_to_ring_varlen.  Sinks
+ * that a sequence's tokens do not reach keep their contents.
+ */
+int swa_prefill_to_sinks(const swa_params_t* p, int32_t n_sink, const int64_t* starts,
+                         const int64_t* lens, const int64_t* pos0, const swa_bf16_t* k,
+                         const swa_bf16_t* v, const float* wk, swa_bf16_t* k_sink,
+                         swa_bf16_t* v_sink, void* stream);
+
 /* Static description of an error code. */
 const char* swa_error_string(int code);
 
