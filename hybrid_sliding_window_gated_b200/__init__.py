@@ -19,6 +19,7 @@ import torch
 __all__ = ["fwd", "fwd_halo", "fwd_fp8", "bwd", "bwd_edges", "bwd_halo", "bwd_noalloc", "bwd_workspace_size", "decode_step", "prefill_to_ring", "prefill_to_ring_varlen",
            "global_fwd", "global_decode_step", "global_decode_workspace_size",
            "sink_fwd", "sink_decode_step", "prefill_to_sinks",
+           "global_decode_shared", "global_decode_shared_workspace_size",
            "get_last_device_error", "SwaError", "Params", "lib", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libswa.so")
@@ -91,6 +92,12 @@ def lib():
         L.swa_sink_decode_step.restype = ctypes.c_int
         L.swa_prefill_to_sinks.argtypes = [P, ctypes.c_int32] + [_vp] * 9
         L.swa_prefill_to_sinks.restype = ctypes.c_int
+        i64 = ctypes.c_int64
+        L.swa_global_decode_shared.argtypes = [P, i64, i64] + [_vp] * 10 + [i64, _vp, _vp,
+                                                                            ctypes.c_size_t, _vp]
+        L.swa_global_decode_shared.restype = ctypes.c_int
+        L.swa_global_decode_shared_workspace_size.argtypes = [P, i64, i64]
+        L.swa_global_decode_shared_workspace_size.restype = ctypes.c_size_t
         L.swa_error_string.argtypes = [ctypes.c_int]
         L.swa_error_string.restype = ctypes.c_char_p
         L.swa_get_last_device_error.argtypes = [_vp, ctypes.POINTER(ctypes.c_int)]
@@ -553,6 +560,48 @@ def prefill_to_sinks(k, v, wk, k_sink, v_sink, starts=None, lens=None, pos0=None
                                     _ptr(k), _ptr(v), _ptr(wk), _ptr(k_sink), _ptr(v_sink),
                                     _stream(stream))
     _check(rc, "swa_prefill_to_sinks")
+
+
+def global_decode_shared_workspace_size(N, Hq, Hkv, prefix_len, cap, *, head_dim=128, rot_dim=42):
+    p = make_params(N, 1, Hq, Hkv, head_dim=head_dim, window=0, rot_dim=rot_dim)
+    return int(lib().swa_global_decode_shared_workspace_size(ctypes.byref(p), prefix_len, cap))
+
+
+def global_decode_shared(pos, q, k_new, v_new, wq, wk, k_prefix, v_prefix, prefix_len, k_cache,
+                         v_cache, *, rot_dim=42, rope_base=1e7, eps=1e-6, scale=0.0, out=None,
+                         workspace=None, flags=0, stream=None):
+    """One decode step of a global layer for sequences that share a prefix
+    (swa_global_decode_shared): k_prefix, v_prefix [1,Hkv,pcap,128] (or without
+    the first axis) hold positions 0 .. prefix_len-1 for all of them, k_cache,
+    v_cache [N,Hkv,cap,128] each sequence's own from prefix_len on; returns
+    o [N,Hq,128]."""
+    N, Hq, D = q.shape
+    Hkv, cap = k_cache.shape[1], k_cache.shape[2]
+    if k_prefix.dim() == 4 and k_prefix.shape[0] != 1:
+        raise ValueError("swa_global_decode_shared: k_prefix holds more than one sequence")
+    pcap = k_prefix.shape[-2]
+    if out is None:
+        out = torch.empty_like(q)
+    p = make_params(N, 1, Hq, Hkv, head_dim=D, window=0, rot_dim=rot_dim, rope_base=rope_base,
+                    eps=eps, scale=scale, flags=flags)
+    nbytes = int(lib().swa_global_decode_shared_workspace_size(ctypes.byref(p), prefix_len, cap))
+    if workspace is None:
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
+    nq, nk = N * Hq * D, N * Hkv * D
+    npre = Hkv * pcap * D if N and prefix_len else 0
+    bf, f32 = torch.bfloat16, torch.float32
+    _need("swa_global_decode_shared", q.device, pos=(pos, torch.int64, N), q=(q, bf, nq),
+          k_new=(k_new, bf, nk), v_new=(v_new, bf, nk), wq=(wq, f32, D if N else 0),
+          wk=(wk, f32, D if N else 0), k_prefix=(k_prefix, bf, npre), v_prefix=(v_prefix, bf, npre),
+          k_cache=(k_cache, bf, nk * cap), v_cache=(v_cache, bf, nk * cap), out=(out, bf, nq),
+          workspace=(workspace, torch.uint8, nbytes if N else 0))
+    rc = lib().swa_global_decode_shared(ctypes.byref(p), prefix_len, pcap, _ptr(k_prefix),
+                                        _ptr(v_prefix), _ptr(pos), _ptr(q), _ptr(k_new),
+                                        _ptr(v_new), _ptr(wq), _ptr(wk), _ptr(k_cache),
+                                        _ptr(v_cache), cap, _ptr(out), _ptr(workspace),
+                                        workspace.numel(), _stream(stream))
+    _check(rc, "swa_global_decode_shared")
+    return out
 
 
 def get_last_device_error(stream=None):

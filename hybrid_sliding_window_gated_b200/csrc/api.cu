@@ -85,7 +85,7 @@ int device_error_word(int** ptr) {
 
 int encode_tmap_4d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                    uint64_t d3, uint32_t box0, uint32_t box1, uint32_t box2, uint32_t box3,
-                   CUtensorMapSwizzle swizzle, bool bytes) {
+                   CUtensorMapSwizzle swizzle, bool bytes, uint64_t pitch1) {
   {
     std::lock_guard<std::mutex> lock(g_mu);
     if (g_encode == nullptr) {
@@ -100,7 +100,8 @@ int encode_tmap_4d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1,
   }
   const cuuint64_t dims[4] = {d0, d1, d2, d3};
   const cuuint64_t eb = bytes ? 1 : 2;
-  const cuuint64_t strides[3] = {d0 * eb, d0 * d1 * eb, d0 * d1 * d2 * eb};  // bytes, dims 1..3
+  if (pitch1 == 0) pitch1 = d1;
+  const cuuint64_t strides[3] = {d0 * eb, d0 * pitch1 * eb, d0 * pitch1 * d2 * eb};  // dims 1..3
   const cuuint32_t box[4] = {box0, box1, box2, box3};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = g_encode(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
@@ -842,6 +843,134 @@ int swa_prefill_to_sinks(const swa_params_t* p, int32_t n_sink, const int64_t* s
   if ((rc = device_error_word(&a.err)) != SWA_OK) return rc;
   fill_inv_freq(p, a.inv_freq);
   return launch_sink_fill(a, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
+
+// -------------------------------------------------------------- shared prefix
+
+extern "C" {
+
+size_t swa_global_decode_shared_workspace_size(const swa_params_t* p, int64_t prefix_len,
+                                               int64_t cache_cap) {
+  if (check_params_global(p, true) != SWA_OK || prefix_len < 0 || cache_cap <= 0 ||
+      prefix_len > (1ll << 30) || cache_cap > (1ll << 30) || p->Hq / p->Hkv > kGlobalMaxGroup ||
+      p->B > (1ll << 24))
+    return 0;
+  return shared_ws(p->B, p->Hkv, p->Hq / p->Hkv, prefix_len, cache_cap).total;
+}
+
+int swa_global_decode_shared(const swa_params_t* p, int64_t prefix_len, int64_t prefix_cap,
+                             const swa_bf16_t* k_prefix, const swa_bf16_t* v_prefix,
+                             const int64_t* pos, const swa_bf16_t* q, const swa_bf16_t* k_new,
+                             const swa_bf16_t* v_new, const float* wq, const float* wk,
+                             swa_bf16_t* k_cache, swa_bf16_t* v_cache, int64_t cache_cap,
+                             swa_bf16_t* o, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  int rc = check_params_global(p, true);
+  if (rc != SWA_OK) return rc;
+  if (cache_cap <= 0 || prefix_len < 0 || prefix_cap < prefix_len) return SWA_ERR_INVALID_ARG;
+  const int G = p->Hq / p->Hkv;
+  if (G > kGlobalMaxGroup || cache_cap > (1ll << 30) || prefix_cap > (1ll << 30) ||
+      p->B > (1ll << 24))
+    return SWA_ERR_UNSUPPORTED;
+  if (p->B == 0) return SWA_OK;
+  if (!pos || !q || !k_new || !v_new || !wq || !wk || !k_cache || !v_cache || !o || !workspace ||
+      (prefix_len > 0 && (!k_prefix || !v_prefix)))
+    return SWA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(pos) & 7u) || !aligned16(q) || !aligned16(k_new) ||
+      !aligned16(v_new) || !aligned16(wq) || !aligned16(wk) || !aligned16(k_cache) ||
+      !aligned16(v_cache) || !aligned16(o) || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+      (prefix_len > 0 && (!aligned16(k_prefix) || !aligned16(v_prefix))))
+    return SWA_ERR_INVALID_ARG;
+  const SharedWs w = shared_ws(p->B, p->Hkv, G, prefix_len, cache_cap);
+  if (workspace_bytes < w.total) return SWA_ERR_INVALID_ARG;
+  int* err = nullptr;
+  if ((rc = device_error_word(&err)) != SWA_OK) return rc;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+
+  SharedPrepArgs pa{};
+  pa.N = static_cast<int>(p->B);
+  pa.Hq = p->Hq;
+  pa.Hkv = p->Hkv;
+  pa.G = G;
+  pa.half_rot = p->rot_dim / 2;
+  pa.rows_pad = w.rows_pad;
+  pa.eps = p->eps;
+  pa.base = prefix_len;
+  pa.cap = cache_cap;
+  pa.pos = pos;
+  pa.q = q;
+  pa.k = k_new;
+  pa.v = v_new;
+  pa.wq = wq;
+  pa.wk = wk;
+  pa.k_cache = k_cache;
+  pa.v_cache = v_cache;
+  pa.qs = reinterpret_cast<uint16_t*>(ws + w.qs);
+  pa.err = err;
+  fill_inv_freq(p, pa.inv_freq);
+
+  PrefixArgs xa{};
+  xa.Hkv = p->Hkv;
+  xa.rows = static_cast<int>(p->B * G);
+  xa.rows_pad = w.rows_pad;
+  xa.pairs = w.pairs;
+  xa.two = w.two;
+  xa.splits = w.splits;
+  xa.ctas_per_head = w.ctas_per_head;
+  xa.key_tiles = w.key_tiles;
+  xa.len = static_cast<int>(prefix_len);
+  xa.scale_log2 = score_scale(p) * 1.4426950408889634f;
+  xa.flags = p->flags;
+  xa.part_o = reinterpret_cast<float*>(ws + w.pre_o);
+  xa.part_ml = reinterpret_cast<float*>(ws + w.pre_ml);
+  xa.err = err;
+
+  GlobalDecArgs a{};
+  a.N = static_cast<int>(p->B);
+  a.Hq = p->Hq;
+  a.Hkv = p->Hkv;
+  a.G = G;
+  a.half_rot = p->rot_dim / 2;
+  a.chunks = static_cast<int>((cache_cap + kGlobalChunk - 1) / kGlobalChunk);
+  a.scale_log2 = xa.scale_log2;
+  a.eps = p->eps;
+  a.cap = cache_cap;
+  a.pos = pos;
+  a.q = q;
+  a.wq = wq;
+  a.part_o = reinterpret_cast<float*>(ws + w.part_o);
+  a.part_ml = reinterpret_cast<float*>(ws + w.part_ml);
+  a.o = o;
+  a.err = err;
+  a.base = prefix_len;
+  a.splits = w.splits;
+  a.rows_pad = w.rows_pad;
+  a.pre_o = xa.part_o;
+  a.pre_ml = xa.part_ml;
+  for (int j = 0; j < kMaxPairs; ++j) a.inv_freq[j] = pa.inv_freq[j];
+
+  // The prefix's tensor maps end at prefix_len: keys past it arrive as zeros.
+  CUtensorMap tq, tkp, tvp, tk, tv;
+  const uint64_t D = kHeadDim, N = p->B;
+  if ((rc = encode_tmap_4d(&tk, k_cache, D, cache_cap, p->Hkv, N, 64, kTile, 1, 1,
+                           CU_TENSOR_MAP_SWIZZLE_128B)) ||
+      (rc = encode_tmap_4d(&tv, v_cache, D, cache_cap, p->Hkv, N, 64, kTile, 1, 1,
+                           CU_TENSOR_MAP_SWIZZLE_128B)))
+    return rc;
+  if (prefix_len > 0 &&
+      ((rc = encode_tmap_4d(&tq, pa.qs, D, w.rows_pad, p->Hkv, 2, 64, kTile, 1, 1,
+                            CU_TENSOR_MAP_SWIZZLE_128B)) ||
+       (rc = encode_tmap_4d(&tkp, k_prefix, D, prefix_len, p->Hkv, 1, 64, kTile, 1, 1,
+                            CU_TENSOR_MAP_SWIZZLE_128B, false, prefix_cap)) ||
+       (rc = encode_tmap_4d(&tvp, v_prefix, D, prefix_len, p->Hkv, 1, 64, kTile, 1, 1,
+                            CU_TENSOR_MAP_SWIZZLE_128B, false, prefix_cap))))
+    return rc;
+  if ((rc = launch_shared_prep(pa, st)) != SWA_OK) return rc;
+  if (prefix_len > 0 && (rc = launch_prefix(tq, tkp, tvp, xa, st)) != SWA_OK) return rc;
+  return launch_shared_suffix(tk, tv, a, st);
 }
 
 }  // extern "C"

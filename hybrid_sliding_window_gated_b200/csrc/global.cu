@@ -39,6 +39,8 @@
 // accumulates across key tiles with no rescaling at all.  Larger weights
 // take an exact two-pass form: a first pass over the key tiles finds each
 // row's maximum (QK^T only), the second uses it.
+#include <atomic>
+
 #include "decode_internal.h"
 #include "global_internal.h"
 #include "launch.cuh"
@@ -626,7 +628,7 @@ struct alignas(1024) DecStage {
 };
 struct alignas(1024) DecSmem {
   DecStage st[kDecStages];
-  uint32_t qa[kGlobalMaxGroup][kQStride];
+  uint32_t qa[2 * kGlobalMaxGroup][kQStride];  // q', then (shared prefix) its remainders
   float scratch[4][kHeadDim];
   float mw[4][kGlobalMaxGroup], lw[4][kGlobalMaxGroup];
   uint64_t full[kDecStages], empty[kDecStages];
@@ -650,7 +652,10 @@ __device__ __forceinline__ void consumers_sync() { named_sync(1, 128); }
 // scores keys 32 w .. 32 w + 31 of each tile with mma.sync (the group's query
 // heads are the M rows, padded to 16), keeps a running maximum, rescales its
 // partial O, and the four warps' partials are merged at the end into the
-// chunk's (max, sum, O) in the workspace.
+// chunk's (max, sum, O) in the workspace.  kShared (a step behind a shared
+// prefix): the caches start at position a.base, and q' and P enter with a second
+// bf16 term each, in the M rows 8-15 that the group's heads leave empty.
+template <bool kShared>
 __global__ void __launch_bounds__(kDecThreads, 1)
     global_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const GlobalDecArgs a) {
@@ -676,7 +681,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   volatile int* abort = &sm.abort;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const long long p = a.pos[n];
+  const long long pa = a.pos[n], p = kShared ? pa - a.base : pa;  // position; its cache slot
   const long long c0 = static_cast<long long>(c) * kGlobalChunk;
   if (p < 0 || p >= a.cap) {  // reported by the cache writer before this kernel
     return;
@@ -719,13 +724,19 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   // q' for heads lw, lw + 4 at position p
   {
     float cs = 1.0f, sn = 0.0f;
-    if (lane < a.half_rot) rope_cos_sin(static_cast<double>(p), a.inv_freq[lane], &cs, &sn);
+    if (lane < a.half_rot) rope_cos_sin(static_cast<double>(pa), a.inv_freq[lane], &cs, &sn);
     for (int h = lw; h < a.G; h += 4) {
       float x[4];
       load4(a.q + (static_cast<long long>(n) * a.Hq + kvh * a.G + h) * kHeadDim + 4 * lane, x);
       norm_rope_row(x, a.wq, a.eps, sm.scratch[lw], lane, a.half_rot, cs, sn);
-      sm.qa[h][2 * lane] = pack_bf16x2(x[0], x[1]);
-      sm.qa[h][2 * lane + 1] = pack_bf16x2(x[2], x[3]);
+      const uint32_t h0 = pack_bf16x2(x[0], x[1]), h1 = pack_bf16x2(x[2], x[3]);
+      sm.qa[h][2 * lane] = h0;
+      sm.qa[h][2 * lane + 1] = h1;
+      if (kShared) {
+        sm.qa[kGlobalMaxGroup + h][2 * lane] = pack_bf16x2(x[0] - bf16_lo(h0), x[1] - bf16_hi(h0));
+        sm.qa[kGlobalMaxGroup + h][2 * lane + 1] =
+            pack_bf16x2(x[2] - bf16_lo(h1), x[3] - bf16_hi(h1));
+      }
     }
   }
   bool ok = true;
@@ -765,20 +776,24 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     const uint32_t kbase = smem_u32(st.k[0]);
 #pragma unroll
     for (int kp2 = 0; kp2 < 4; ++kp2) {
-      uint32_t qa0[2], qa2[2];
+      uint32_t qa0[2], qa2[2], qa1[2] = {0u, 0u}, qa3[2] = {0u, 0u};
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int kk = 2 * kp2 + e;
         qa0[e] = row_ok ? sm.qa[grp][8 * kk + tig] : 0u;
         qa2[e] = row_ok ? sm.qa[grp][8 * kk + 4 + tig] : 0u;
+        if (kShared) {
+          qa1[e] = row_ok ? sm.qa[kGlobalMaxGroup + grp][8 * kk + tig] : 0u;
+          qa3[e] = row_ok ? sm.qa[kGlobalMaxGroup + grp][8 * kk + 4 + tig] : 0u;
+        }
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint32_t b[4];
         const int slot = 32 * lw + 8 * j + (lane & 7);
         ldsm_x4(kbase + ring_off(slot, 4 * kp2 + (lane >> 3)), b);
-        mma_16816(acc[j], qa0[0], 0u, qa2[0], 0u, b[0], b[1]);
-        mma_16816(acc[j], qa0[1], 0u, qa2[1], 0u, b[2], b[3]);
+        mma_16816(acc[j], qa0[0], qa1[0], qa2[0], qa3[0], b[0], b[1]);
+        mma_16816(acc[j], qa0[1], qa1[1], qa2[1], qa3[1], b[2], b[3]);
       }
     }
     // running maximum and rescale (log2 units)
@@ -788,6 +803,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const long long key = key0 + 32 * lw + 8 * j + 2 * tig + e;
+        if (kShared) acc[j][e] += acc[j][e + 2];
         acc[j][e] = key <= p ? acc[j][e] * a.scale_log2 : -INFINITY;
         tm = fmaxf(tm, acc[j][e]);
       }
@@ -803,26 +819,34 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     for (int nd = 0; nd < 16; ++nd) {
       oacc[nd][0] *= corr;
       oacc[nd][1] *= corr;
+      if (kShared) {
+        oacc[nd][2] *= corr;
+        oacc[nd][3] *= corr;
+      }
     }
-    uint32_t pa[4];
+    uint32_t pf[4], pr[4];  // P as bf16, and what that left over
     float ls = 0.0f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float p0 = ex2_approx(acc[j][0] - mu), p1 = ex2_approx(acc[j][1] - mu);
       ls += p0 + p1;
-      pa[j] = pack_bf16x2(p0, p1);
+      pf[j] = pack_bf16x2(p0, p1);
+      pr[j] = kShared ? pack_bf16x2(p0 - bf16_lo(pf[j]), p1 - bf16_hi(pf[j])) : 0u;
     }
     ls += __shfl_xor_sync(0xffffffffu, ls, 1);
     ls += __shfl_xor_sync(0xffffffffu, ls, 2);
     l += ls;
-    if (!row_ok) pa[0] = pa[1] = pa[2] = pa[3] = 0u;
+    if (!row_ok) {
+      pf[0] = pf[1] = pf[2] = pf[3] = 0u;
+      pr[0] = pr[1] = pr[2] = pr[3] = 0u;
+    }
     const uint32_t vbase = smem_u32(st.v[0]);
 #pragma unroll
     for (int nd = 0; nd < 16; ++nd) {
       uint32_t b[4];
       ldsm_x4_trans(vbase + ring_off(32 * lw + lane, nd), b);
-      mma_16816(oacc[nd], pa[0], 0u, pa[1], 0u, b[0], b[1]);
-      mma_16816(oacc[nd], pa[2], 0u, pa[3], 0u, b[2], b[3]);
+      mma_16816(oacc[nd], pf[0], pr[0], pf[1], pr[1], b[0], b[1]);
+      mma_16816(oacc[nd], pf[2], pr[2], pf[3], pr[3], b[2], b[3]);
     }
     __syncwarp();
     // every warp's reads of this stage are done before the producer refills it
@@ -841,7 +865,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 #pragma unroll
     for (int nd = 0; nd < 16; ++nd)
       *reinterpret_cast<float2*>(part + (lw * kGlobalMaxGroup + grp) * kOStride + 8 * nd + 2 * tig) =
-          make_float2(oacc[nd][0], oacc[nd][1]);
+          kShared ? make_float2(oacc[nd][0] + oacc[nd][2], oacc[nd][1] + oacc[nd][3])
+                  : make_float2(oacc[nd][0], oacc[nd][1]);
   }
   consumers_sync();
   if (!ok) return;
@@ -873,7 +898,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   }
 }
 
-// One warp per (sequence, query head): o = sum_c 2^(m_c - m) O_c / sum_c 2^(m_c - m) l_c.
+// One warp per (sequence, query head): o = sum_c 2^(m_c - m) O_c / sum_c 2^(m_c - m) l_c,
+// over the chunks of the sequence's cache and (kShared) the splits of the prefix.
+template <bool kShared>
 __global__ void __launch_bounds__(256) global_combine_kernel(const GlobalDecArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -882,12 +909,18 @@ __global__ void __launch_bounds__(256) global_combine_kernel(const GlobalDecArgs
   if (r >= static_cast<long long>(a.N) * a.Hq) return;
   const int n = static_cast<int>(r / a.Hq), hq = static_cast<int>(r % a.Hq);
   const int kvh = hq / a.G, h = hq - kvh * a.G;
-  const long long p = a.pos[n];
+  const long long p = kShared ? a.pos[n] - a.base : a.pos[n];
   if (p < 0 || p >= a.cap) return;
   const int nc = static_cast<int>(p / kGlobalChunk) + 1;
   const long long base = (static_cast<long long>(n) * a.Hkv + kvh) * a.chunks;
   float mx = -INFINITY;
   for (int c = 0; c < nc; ++c) mx = fmaxf(mx, a.part_ml[((base + c) * a.G + h) * 2]);
+  const long long pre = kShared ? static_cast<long long>(kvh) * a.splits * a.rows_pad +
+                                      static_cast<long long>(n) * a.G + h
+                                : 0;
+  if (kShared)
+    for (int c = 0; c < a.splits; ++c)
+      mx = fmaxf(mx, a.pre_ml[(pre + static_cast<long long>(c) * a.rows_pad) * 2]);
   float y[4] = {0.f, 0.f, 0.f, 0.f}, lsum = 0.0f;
   for (int c = 0; c < nc; ++c) {
     const long long slot = (base + c) * a.G + h;
@@ -899,6 +932,20 @@ __global__ void __launch_bounds__(256) global_combine_kernel(const GlobalDecArgs
     y[1] += f * v4.y;
     y[2] += f * v4.z;
     y[3] += f * v4.w;
+  }
+  if (kShared) {
+    for (int c = 0; c < a.splits; ++c) {
+      const long long slot = pre + static_cast<long long>(c) * a.rows_pad;
+      const float2 ml = *reinterpret_cast<const float2*>(a.pre_ml + slot * 2);
+      if (ml.x == -INFINITY) continue;  // a split without keys: its O was not written
+      const float f = ex2_approx(ml.x - mx);
+      lsum += f * ml.y;
+      const float4 v4 = *reinterpret_cast<const float4*>(a.pre_o + slot * kHeadDim + 4 * lane);
+      y[0] += f * v4.x;
+      y[1] += f * v4.y;
+      y[2] += f * v4.z;
+      y[3] += f * v4.w;
+    }
   }
   const float il = 1.0f / lsum;
   *reinterpret_cast<uint2*>(a.o + r * kHeadDim + 4 * lane) =
@@ -953,28 +1000,46 @@ int launch_global_fwd(int rot_dim, const CUtensorMap& tq, const CUtensorMap& tk,
   }
 }
 
-int launch_global_decode(const CUtensorMap& tk, const CUtensorMap& tv, const GlobalDecArgs& a,
-                         cudaStream_t stream) {
+}  // namespace swa
+
+namespace swa {
+namespace glb {
+
+template <bool kShared>
+int launch_decode_impl(const CUtensorMap& tk, const CUtensorMap& tv, const GlobalDecArgs& a,
+                       cudaStream_t stream) {
   DeviceInfo di;
   int rc = current_device_info(&di);
   if (rc != SWA_OK) return rc;
-  const size_t smem = sizeof(glb::DecSmem) + 1024;
-  static int configured_device = -1;
-  if (configured_device != di.device) {
-    cudaError_t e = cudaFuncSetAttribute(glb::global_decode_kernel,
+  const size_t smem = sizeof(DecSmem) + 1024;
+  static std::atomic<int> configured[64];  // per device
+  if (!configured[di.device].load(std::memory_order_acquire)) {
+    cudaError_t e = cudaFuncSetAttribute(global_decode_kernel<kShared>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return map_cuda_error(e);
-    configured_device = di.device;
+    configured[di.device].store(1, std::memory_order_release);
   }
   const long long items = static_cast<long long>(a.N) * a.Hkv * a.chunks;
   if (items > 0x7fffffffLL) return SWA_ERR_UNSUPPORTED;
-  rc = launch_dependent(glb::global_decode_kernel, static_cast<unsigned>(items), glb::kDecThreads,
+  rc = launch_dependent(global_decode_kernel<kShared>, static_cast<unsigned>(items), kDecThreads,
                         smem, stream, tk, tv, a);
   if (rc != SWA_OK) return rc;
   const long long rows = static_cast<long long>(a.N) * a.Hq;
-  return launch_dependent(glb::global_combine_kernel, static_cast<unsigned>((rows + 7) / 8), 256, 0,
-                          stream, a);
+  return launch_dependent(global_combine_kernel<kShared>, static_cast<unsigned>((rows + 7) / 8),
+                          256, 0, stream, a);
+}
+
+}  // namespace glb
+
+int launch_global_decode(const CUtensorMap& tk, const CUtensorMap& tv, const GlobalDecArgs& a,
+                         cudaStream_t stream) {
+  return glb::launch_decode_impl<false>(tk, tv, a, stream);
+}
+
+int launch_shared_suffix(const CUtensorMap& tk, const CUtensorMap& tv, const GlobalDecArgs& a,
+                         cudaStream_t stream) {
+  return glb::launch_decode_impl<true>(tk, tv, a, stream);
 }
 
 }  // namespace swa

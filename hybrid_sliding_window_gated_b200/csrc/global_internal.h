@@ -59,8 +59,64 @@ struct GlobalDecArgs {
   float* part_ml;       // [N, Hkv, chunks, G, 2] fp32: row maximum (log2 units), row sum
   uint16_t* o;          // [N, Hq, D]
   int* err;
+  // Shared prefix (swa_global_decode_shared): the caches hold positions base,
+  // base + 1, ..; the prefix's partial results come from prefix_attn_kernel.
+  long long base;
+  int splits;             // prefix partials per query row (0: no prefix)
+  int rows_pad;           // query rows per KV head, rounded up to 128
+  const float* pre_o;     // [Hkv, splits, rows_pad, D] fp32
+  const float* pre_ml;    // [Hkv, splits, rows_pad, 2] fp32
   double inv_freq[kMaxPairs];
 };
+
+// The new tokens of a shared-prefix step: k', v into the sequences' caches, and
+// q' into the workspace as the bf16 of its value and of what that left over.
+struct SharedPrepArgs {
+  int N, Hq, Hkv, G;
+  int half_rot;
+  int rows_pad;
+  float eps;
+  long long base, cap;
+  const int64_t* pos;
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  const float* wq;
+  const float* wk;
+  uint16_t* k_cache;
+  uint16_t* v_cache;
+  uint16_t* qs;           // [2, Hkv, rows_pad, D]: value, remainder
+  int* err;
+  double inv_freq[kMaxPairs];
+};
+
+struct PrefixArgs {
+  int Hkv, rows, rows_pad;
+  int pairs;              // 256-row pairs of row tiles (two = 1), or 1 row tile (two = 0)
+  int two;                // 1: the two regions hold different rows; 0: different keys
+  int splits;             // partial results per row
+  int ctas_per_head;      // splits of the key tiles over CTAs
+  int key_tiles;          // 128-key tiles of the prefix
+  int len;                // prefix length
+  float scale_log2;
+  int flags;
+  float* part_o;
+  float* part_ml;
+  int* err;
+};
+
+// Workspace of the shared-prefix step, in bytes from its start.
+struct SharedWs {
+  int rows_pad, two, pairs, ctas_per_head, splits, key_tiles;
+  size_t qs, pre_o, pre_ml, part_o, part_ml, total;
+};
+SharedWs shared_ws(long long N, int Hkv, int G, long long prefix, long long cap);
+
+int launch_shared_prep(const SharedPrepArgs& a, cudaStream_t stream);
+int launch_prefix(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                  const PrefixArgs& a, cudaStream_t stream);
+int launch_shared_suffix(const CUtensorMap& tk, const CUtensorMap& tv, const GlobalDecArgs& a,
+                         cudaStream_t stream);
 
 inline size_t global_decode_ws_bytes(long long N, int Hkv, int G, long long cap) {
   const long long chunks = (cap + kGlobalChunk - 1) / kGlobalChunk;

@@ -41,10 +41,11 @@ struct DeviceInfo {
 int current_device_info(DeviceInfo* info);
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point: bf16
-// elements, or single bytes when `bytes` is set.
+// elements, or single bytes when `bytes` is set.  The tensor is contiguous but
+// for dim 2, whose steps are pitch1 rows of dim 0 (0: d1 rows).
 int encode_tmap_4d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                    uint64_t d3, uint32_t box0, uint32_t box1, uint32_t box2, uint32_t box3,
-                   CUtensorMapSwizzle swizzle, bool bytes = false);
+                   CUtensorMapSwizzle swizzle, bool bytes = false, uint64_t pitch1 = 0);
 
 // tkh, tvh: tensor maps of the halo K and V [B, W-1, Hkv, D] (used only when
 // a.halo is set; any valid map otherwise).

@@ -368,6 +368,35 @@ int swa_prefill_to_sinks(const swa_params_t* p, int32_t n_sink, const int64_t* s
                          const swa_bf16_t* v, const float* wk, swa_bf16_t* k_sink,
                          swa_bf16_t* v_sink, void* stream);
 
+/*
+ * One decode step of a global layer for p->B sequences that continue one common
+ * prefix of prefix_len tokens (several samples of one prompt, requests behind one
+ * system prompt).  The prefix's keys and values lie in one cache for all of them,
+ * k_prefix, v_prefix [Hkv, prefix_cap, D] bf16, slots 0 .. prefix_len - 1 as
+ * swa_global_fwd writes them for one batch row (prefix_cap >= prefix_len >= 0; both
+ * may be NULL when prefix_len is 0); they are read once per step, not once per
+ * sequence.  Each sequence's own tokens lie in k_cache, v_cache [B, Hkv, cache_cap,
+ * D]: position x in slot x - prefix_len.  pos: [B] int64 device array, prefix_len <=
+ * pos < prefix_len + cache_cap (else that sequence is skipped and
+ * swa_get_last_device_error returns SWA_ERR_INVALID_ARG); slot pos[n] - prefix_len
+ * receives k' and v_new, then q' attends over the prefix and the sequence's slots up
+ * to that one.  Slots past it, and prefix slots from prefix_len on, may hold anything.
+ * q, k_new, v_new, wq, wk, o as in swa_global_decode_step; `workspace`: caller-owned
+ * device scratch of swa_global_decode_shared_workspace_size bytes, 256-byte aligned,
+ * which no other call may use at the same time.  p->window must be 0; Hq / Hkv <= 8.
+ */
+int swa_global_decode_shared(const swa_params_t* p, int64_t prefix_len, int64_t prefix_cap,
+                             const swa_bf16_t* k_prefix, const swa_bf16_t* v_prefix,
+                             const int64_t* pos, const swa_bf16_t* q, const swa_bf16_t* k_new,
+                             const swa_bf16_t* v_new, const float* wq, const float* wk,
+                             swa_bf16_t* k_cache, swa_bf16_t* v_cache, int64_t cache_cap,
+                             swa_bf16_t* o, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* Bytes of scratch swa_global_decode_shared needs (0 if unsupported). */
+size_t swa_global_decode_shared_workspace_size(const swa_params_t* p, int64_t prefix_len,
+                                               int64_t cache_cap);
+
 /* Static description of an error code. */
 const char* swa_error_string(int code);
 
