@@ -18,7 +18,7 @@ import torch
 
 __all__ = ["fwd", "fwd_halo", "fwd_fp8", "bwd", "bwd_edges", "bwd_halo", "bwd_noalloc", "bwd_workspace_size", "decode_step", "prefill_to_ring", "prefill_to_ring_varlen",
            "global_fwd", "global_decode_step", "global_decode_workspace_size",
-           "sink_fwd", "sink_decode_step", "prefill_to_sinks",
+           "sink_fwd", "sink_bwd", "sink_bwd_workspace_size", "sink_decode_step", "prefill_to_sinks",
            "global_decode_shared", "global_decode_shared_workspace_size",
            "get_last_device_error", "SwaError", "Params", "lib", "LIB_PATH"]
 
@@ -88,6 +88,10 @@ def lib():
         L.swa_global_decode_step.restype = ctypes.c_int
         L.swa_sink_fwd.argtypes = [P, ctypes.c_int32] + [_vp] * 9
         L.swa_sink_fwd.restype = ctypes.c_int
+        L.swa_sink_bwd.argtypes = [P, ctypes.c_int32] + [_vp] * 16 + [ctypes.c_size_t, _vp]
+        L.swa_sink_bwd.restype = ctypes.c_int
+        L.swa_sink_bwd_workspace_size.argtypes = [P, ctypes.c_int32]
+        L.swa_sink_bwd_workspace_size.restype = ctypes.c_size_t
         L.swa_sink_decode_step.argtypes = [P, ctypes.c_int32] + [_vp] * 13
         L.swa_sink_decode_step.restype = ctypes.c_int
         L.swa_prefill_to_sinks.argtypes = [P, ctypes.c_int32] + [_vp] * 9
@@ -511,6 +515,37 @@ def sink_fwd(q, k, v, g, wq, wk, n_sink, *, window=128, rot_dim=42, rope_base=1e
                             _ptr(wk), _ptr(out), _ptr(lse), _stream(stream))
     _check(rc, "swa_sink_fwd")
     return (out, lse) if lse is not None else out
+
+
+def sink_bwd_workspace_size(B, T, Hq, Hkv, n_sink, *, head_dim=128, window=128, rot_dim=42):
+    p = make_params(B, T, Hq, Hkv, head_dim=head_dim, window=window, rot_dim=rot_dim)
+    return int(lib().swa_sink_bwd_workspace_size(ctypes.byref(p), n_sink))
+
+
+def sink_bwd(q, k, v, g, wq, wk, o, lse, dO, n_sink, *, window=128, rot_dim=42, rope_base=1e4,
+             eps=1e-6, scale=0.0, workspace=None, grads=None, flags=0, stream=None):
+    """Gradients (dq, dk, dv, dg, dwq, dwk) of sum(o * dO) for :func:`sink_fwd`, whose
+    outputs o and lse are arguments (swa_sink_bwd)."""
+    B, T, Hq, D = q.shape
+    Hkv = k.shape[2]
+    p = make_params(B, T, Hq, Hkv, head_dim=D, window=window, rot_dim=rot_dim,
+                    rope_base=rope_base, eps=eps, scale=scale, flags=flags)
+    if grads is None:
+        grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(g),
+                 torch.zeros(D, dtype=torch.float32, device=q.device),
+                 torch.zeros(D, dtype=torch.float32, device=q.device))
+    dq, dk, dv, dg, dwq, dwk = grads
+    nbytes = int(lib().swa_sink_bwd_workspace_size(ctypes.byref(p), n_sink))
+    if workspace is None:
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
+    _need_bwd("swa_sink_bwd", q, k, v, g, wq, wk, lse, dO, grads,
+              o=(o, torch.bfloat16, B * T * Hq * D), workspace=(workspace, torch.uint8, nbytes))
+    rc = lib().swa_sink_bwd(ctypes.byref(p), n_sink, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(wq),
+                            _ptr(wk), _ptr(o), _ptr(lse), _ptr(dO), _ptr(dq), _ptr(dk), _ptr(dv),
+                            _ptr(dg), _ptr(dwq), _ptr(dwk), _ptr(workspace), workspace.numel(),
+                            _stream(stream))
+    _check(rc, "swa_sink_bwd")
+    return grads
 
 
 def sink_decode_step(pos, q, k_new, v_new, g, wq, wk, k_cache, v_cache, k_sink, v_sink, *,

@@ -751,6 +751,78 @@ int swa_sink_fwd(const swa_params_t* p, int32_t n_sink, const swa_bf16_t* q, con
   return launch_sink_fwd(a, static_cast<cudaStream_t>(stream));
 }
 
+size_t swa_sink_bwd_workspace_size(const swa_params_t* p, int32_t n_sink) {
+  if (check_params_sink(p, n_sink, false) != SWA_OK) return 0;
+  return sink_bwd_ws(p->B, p->T, p->Hq, p->Hkv, n_sink).total;
+}
+
+int swa_sink_bwd(const swa_params_t* p, int32_t n_sink, const swa_bf16_t* q, const swa_bf16_t* k,
+                 const swa_bf16_t* v, const swa_bf16_t* g, const float* wq, const float* wk,
+                 const swa_bf16_t* o, const float* lse, const swa_bf16_t* dO, swa_bf16_t* dq,
+                 swa_bf16_t* dk, swa_bf16_t* dv, swa_bf16_t* dg, float* dwq, float* dwk,
+                 void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_params_sink(p, n_sink, false);
+  if (rc != SWA_OK) return rc;
+  if (p->B == 0 || p->T == 0) return SWA_OK;
+  if (!q || !k || !v || !g || !wq || !wk || !o || !lse || !dO || !dq || !dk || !dv || !dg ||
+      !dwq || !dwk || !workspace)
+    return SWA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(g) || !aligned16(wq) ||
+      !aligned16(wk) || !aligned16(o) || !aligned16(dO) || !aligned16(dq) || !aligned16(dk) ||
+      !aligned16(dv) || !aligned16(dg) || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
+      (reinterpret_cast<uintptr_t>(dwq) & 3u) || (reinterpret_cast<uintptr_t>(dwk) & 3u) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return SWA_ERR_INVALID_ARG;
+  const SinkBwdWs w = sink_bwd_ws(p->B, p->T, p->Hq, p->Hkv, n_sink);
+  if (workspace_bytes < w.total) return SWA_ERR_INVALID_ARG;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  SinkBwdArgs a{};
+  a.B = static_cast<int>(p->B);
+  a.T = static_cast<int>(p->T);
+  a.tiles = static_cast<int>((p->T + kSinkTile - 1) / kSinkTile);
+  a.Tp = a.tiles * kSinkTile;
+  a.Hq = p->Hq;
+  a.Hkv = p->Hkv;
+  a.G = p->Hq / p->Hkv;
+  a.n_sink = n_sink;
+  a.half_rot = p->rot_dim / 2;
+  a.chunks = n_sink > 0 ? (a.Tp + kSinkChunk - 1) / kSinkChunk : 0;
+  a.scale = score_scale(p);
+  a.scale_log2 = a.scale * 1.4426950408889634f;
+  a.eps = p->eps;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.g = g;
+  a.o = o;
+  a.dO = dO;
+  a.lse = lse;
+  a.wq = wq;
+  a.wk = wk;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.dg = dg;
+  a.dwq = dwq;
+  a.dwk = dwk;
+  a.rot = reinterpret_cast<float2*>(ws + w.rot);
+  a.kr = ws + w.kr;
+  a.vr = ws + w.vr;
+  a.va = reinterpret_cast<float*>(ws + w.va);
+  a.qr = ws + w.qr;
+  a.dr = ws + w.dr;
+  a.row = reinterpret_cast<float4*>(ws + w.row);
+  a.bmin = reinterpret_cast<float*>(ws + w.bmin);
+  a.amin = reinterpret_cast<float*>(ws + w.amin);
+  a.dwq_part = reinterpret_cast<float*>(ws + w.dwq);
+  a.dwk_part = reinterpret_cast<float*>(ws + w.dwk);
+  a.sink_part = reinterpret_cast<float*>(ws + w.part);
+  a.sink_sum = reinterpret_cast<float*>(ws + w.sum);
+  if ((rc = device_error_word(&a.err)) != SWA_OK) return rc;
+  fill_inv_freq(p, a.inv_freq);
+  return launch_sink_bwd(a, static_cast<cudaStream_t>(stream));
+}
+
 int swa_sink_decode_step(const swa_params_t* p, int32_t n_sink, const int64_t* pos,
                          const swa_bf16_t* q, const swa_bf16_t* k_new, const swa_bf16_t* v_new,
                          const swa_bf16_t* g, const float* wq, const float* wk,

@@ -77,6 +77,85 @@ int launch_sink_decode(const CUtensorMap& tk, const CUtensorMap& tv, const CUten
                        const CUtensorMap& tvs, SinkDecArgs a, cudaStream_t stream);
 int launch_sink_fill(const SinkFillArgs& a, cudaStream_t stream);
 
+// Backward.  Everything in `ws` is scratch, laid out by sink_bwd_ws; Tp is T
+// rounded up to a whole tile, and rows past T hold zeros.
+struct SinkBwdArgs {
+  int B, T, Tp, Hq, Hkv, G;
+  int n_sink;
+  int half_rot;
+  int tiles;              // kSinkTile-token tiles per sequence
+  int chunks;             // token chunks of the sinks' pass per (batch row, KV head)
+  float scale, scale_log2, eps;
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  const uint16_t* g;
+  const uint16_t* o;
+  const uint16_t* dO;
+  const float* lse;       // [B, Hq, T]
+  const float* wq;
+  const float* wk;
+  uint16_t* dq;
+  uint16_t* dk;
+  uint16_t* dv;
+  uint16_t* dg;
+  float* dwq;
+  float* dwk;
+  // Operand rows are 256 bytes of fp16 whose 16-byte chunk c lies at c ^ (t & 7).
+  float2* rot;            // [Tp, kMaxPairs]: rot(t w_j)
+  uint8_t* kr;            // [B, Hkv, Tp] rows k' / ck, rope order
+  uint8_t* vr;            // [B, Hkv, Tp] rows v 2^a, split order
+  float* va;              // [B, Hkv, Tp]: a, the exponent that brings max|v| into [1, 2)
+  uint8_t* qr;            // [B, Hq, Tp] rows q' / cq, rope order
+  uint8_t* dr;            // [B, Hq, Tp] rows dA 2^b, split order
+  float4* row;            // [B, Hq, Tp]: lse log2(e), D 2^b, b
+  float* bmin;            // [B, Hq, Tp / 16]: least b of 16 rows
+  float* amin;            // [B, Hkv, tiles]: least a of the keys the tile's queries may see
+  float* dwq_part;        // [B Hkv tiles, D]
+  float* dwk_part;
+  float* sink_part;       // [B, Hkv, chunks, 2, kMaxSink, D]: dk' (rope order), dv (split order)
+  float* sink_sum;        // [B, Hkv, 2, kMaxSink, D]
+  int* err;
+  double inv_freq[kMaxPairs];
+};
+
+// Tokens per CTA of the sinks' pass.
+constexpr int kSinkChunk = 512;
+
+struct SinkBwdWs {
+  size_t rot, kr, vr, va, qr, dr, row, bmin, amin, dwq, dwk, part, sum, total;
+};
+inline SinkBwdWs sink_bwd_ws(long long B, long long T, int Hq, int Hkv, int n_sink) {
+  const size_t Tp = static_cast<size_t>((T + kSinkTile - 1) / kSinkTile) * kSinkTile;
+  const size_t tiles = Tp / kSinkTile, hk = static_cast<size_t>(B) * Hkv;
+  const size_t hq = static_cast<size_t>(B) * Hq;
+  const size_t chunks = n_sink > 0 ? (Tp + kSinkChunk - 1) / kSinkChunk : 0;
+  SinkBwdWs w{};
+  size_t at = 0;
+  const auto take = [&at](size_t n) {
+    const size_t r = at;
+    at = (at + n + 255) & ~static_cast<size_t>(255);
+    return r;
+  };
+  w.rot = take(Tp * kMaxPairs * 8);
+  w.kr = take(hk * Tp * 256);
+  w.vr = take(hk * Tp * 256);
+  w.va = take(hk * Tp * 4);
+  w.qr = take(hq * Tp * 256);
+  w.dr = take(hq * Tp * 256);
+  w.row = take(hq * Tp * 16);
+  w.bmin = take(hq * Tp / 16 * 4);
+  w.amin = take(hk * tiles * 4);
+  w.dwq = take(hk * tiles * kHeadDim * 4);
+  w.dwk = take(hk * tiles * kHeadDim * 4);
+  w.part = take(hk * chunks * 2 * kMaxSink * kHeadDim * 4);
+  w.sum = take(n_sink > 0 ? hk * 2 * kMaxSink * kHeadDim * 4 : 0);
+  w.total = at;
+  return w;
+}
+
+int launch_sink_bwd(const SinkBwdArgs& a, cudaStream_t stream);
+
 int launch_sink_fwd(const SinkFwdArgs& a, cudaStream_t stream);
 
 }  // namespace swa

@@ -340,6 +340,26 @@ int swa_sink_fwd(const swa_params_t* p, int32_t n_sink, const swa_bf16_t* q, con
                  swa_bf16_t* o, float* lse, void* stream);
 
 /*
+ * Backward of swa_sink_fwd: the gradients of swa_bwd, given the forward's output o
+ * [B,T,Hq,D] bf16 (where swa_bwd recomputes the attention output) beside its lse, and
+ * the upstream gradient dO.  Writes dq, dk, dv, dg (bf16) and ADDS the weight
+ * gradients into dwq, dwk [D] (fp32; the caller zeroes them).  Sums are made in a
+ * fixed order: equal inputs give equal bits.  Gradients and values of any finite
+ * magnitude are carried (per-row power-of-two scales); inputs that are not finite
+ * reach the gradients of the tokens around them.  `workspace`: caller-owned device
+ * scratch of swa_sink_bwd_workspace_size bytes, 256-byte aligned.  Pointers 16-byte
+ * aligned; errors as swa_fwd.
+ */
+int swa_sink_bwd(const swa_params_t* p, int32_t n_sink, const swa_bf16_t* q, const swa_bf16_t* k,
+                 const swa_bf16_t* v, const swa_bf16_t* g, const float* wq, const float* wk,
+                 const swa_bf16_t* o, const float* lse, const swa_bf16_t* dO, swa_bf16_t* dq,
+                 swa_bf16_t* dk, swa_bf16_t* dv, swa_bf16_t* dg, float* dwq, float* dwk,
+                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of scratch swa_sink_bwd needs for these parameters (0 if unsupported). */
+size_t swa_sink_bwd_workspace_size(const swa_params_t* p, int32_t n_sink);
+
+/*
  * One decode step with sinks: swa_decode_step plus the sink caches k_sink,
  * v_sink [B,Hkv,n_sink,D] bf16 (may be NULL when n_sink is 0), slot s holding
  * k' and v of position s.  The new token at position pos[n] attends over the
