@@ -4,20 +4,22 @@
 // With s = sigmoid(g), A the attention output before the gate, P_ij the
 // probabilities and x . y a sum over the 128 dims:
 //   dg_i  = dO_i A_i s (1 - s) = dO_i o_i (1 - s)
-//   dA_i  = dO_i s,      D_i = dA_i . A_i = dO_i . o_i
+//   dA_i  = dO_i s,      D_i = dA_i . A_i = sum_j P_ij dP_ij
 //   P_ij  = exp(scale q'_i . k'_j - lse_i),   dP_ij = dA_i . v_j
 //   dS_ij = P_ij (dP_ij - D_i)
 //   dq'_i = scale sum_j dS_ij k'_j,  dk'_j = scale sum_i dS_ij q'_i,
 //   dv_j  = sum_i P_ij dA_i
 // and from dx' (x = q or k) back through RoPE and the norm, with u = x / rms:
 //   du = w RoPE^-1(dx'),  dx = (du - u mean(du u)) / rms,  dw = sum RoPE^-1(dx') u.
-// o is the forward's bf16 output: it gives dg and D without a second P V.
+// o is the forward's bf16 output: it gives dg without a second P V.  D could come
+// from o too, but dP - D cancels where a row's probability sits on few keys (a
+// sequence's first tokens), and o's rounding would remain.
 //
 // Kernels, each waiting for the one before it on the stream:
 //   sink_bwd_kv_kernel    k' and v as fp16 operand rows; the table of rotations.
+//   sink_bwd_rows_kernel  q' and dA as operand rows, and dg.
 //   sink_bwd_q_kernel     query-major: 16 queries of one head per warp step, nine
-//                         band blocks and the sinks: S, dP, dQ.  Writes dq, dg and
-//                         the operand rows q' and dA for the next two.
+//                         band blocks and the sinks: S, dP, D, dQ.  Writes dq and D.
 //   sink_bwd_sink_kernel  the sinks' dk' and dv: every query contributes to the same
 //                         16 keys, so chunks of 512 tokens make partial sums, and
 //   sink_bwd_sum_kernel   adds them up in a fixed order.
@@ -56,10 +58,6 @@ __device__ __forceinline__ float scale_exp(float m) {
   const int e = static_cast<int>((__float_as_uint(m) >> 23) & 255u) - 127;
   return static_cast<float>(max(-100, min(100, -e)));
 }
-// 2^x for a whole x in [-126, 127]
-__device__ __forceinline__ float pow2i(float x) {
-  return __uint_as_float(static_cast<uint32_t>(static_cast<int>(x) + 127) << 23);
-}
 // v 2^x for whole x in [-252, 254], in two steps
 __device__ __forceinline__ float scale2(float v, float x) {
   const float h = truncf(0.5f * x);
@@ -73,21 +71,6 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
           "r"(smem_u32(dst)),
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
-}
-
-// The largest |w| of the norm weights, by the 32 lanes of a warp.
-__device__ __forceinline__ float warp_absmax(const float* w, int lane) {
-  float m = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(__ldg(w + lane + 32 * i)));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  return m;
-}
-
-__device__ __forceinline__ void pdl_start() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ------------------------------------------------------------- operand rows
@@ -113,157 +96,291 @@ __global__ void __launch_bounds__(256) sink_bwd_kv_kernel(const SinkBwdArgs a) {
     w_rest = make_float4(w.x * ick, w.y * ick, w.z * ick, w.w * ick);
   }
   const bool real = t < a.T;
-  for (int h = 0; h < a.Hkv; ++h) {
-    const long long src = ((static_cast<long long>(b) * a.T + t) * a.Hkv + h) * kHeadDim;
-    const long long dst = (static_cast<long long>(b) * a.Hkv + h) * a.Tp + t;
-    const KRow x = load_k_row(real ? a.k + src : nullptr, lane, dlo, dhi);
-    // row index t & 7 selects the chunk swizzle; the row itself starts at dst
-    store_k_row(a.kr + (dst - (t & 7)) * kRowBytes, t & 7, x, lane, w_lo, w_hi, w_rest, rot, a.eps);
-    uint2 vv = make_uint2(0u, 0u);
-    if (real) vv = __ldg(reinterpret_cast<const uint2*>(a.v + src + 4 * lane));
-    const float v0 = bf16_lo(vv.x), v1 = bf16_hi(vv.x), v2 = bf16_lo(vv.y), v3 = bf16_hi(vv.y);
-    float m = fmaxf(fmaxf(fabsf(v0), fabsf(v1)), fmaxf(fabsf(v2), fabsf(v3)));
+  constexpr int kN = 4;  // heads at a time (their rows lie next to each other)
+  for (int h0 = 0; h0 < a.Hkv; h0 += kN) {
+    KRow x[kN][1];
+    uint2 v[kN];
+    float m[kN];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float e = scale_exp(m), f = pow2i(e);
-    // dims 4 lane .. + 3 = 32 m + 8 c + 2 q (q = 0 or 2): words q and q + 1
-    const int md = lane >> 3, c = (lane & 7) >> 1, q = 2 * (lane & 1);
-    uint8_t* row = a.vr + (dst - (t & 7)) * kRowBytes;
-    *reinterpret_cast<uint32_t*>(row + row_off(t & 7, 4 * md + q) + 4 * c) =
-        pack_f16x2(v0 * f, v1 * f);
-    *reinterpret_cast<uint32_t*>(row + row_off(t & 7, 4 * md + q + 1) + 4 * c) =
-        pack_f16x2(v2 * f, v3 * f);
-    if (lane == 0) a.va[dst] = e;
+    for (int e = 0; e < kN; ++e) {
+      const bool have = real && h0 + e < a.Hkv;
+      const long long src = ((static_cast<long long>(b) * a.T + t) * a.Hkv + h0 + e) * kHeadDim;
+      x[e][0] = load_k_row(have ? a.k + src : nullptr, lane, dlo, dhi);
+      v[e] = have ? __ldg(reinterpret_cast<const uint2*>(a.v + src + 4 * lane))
+                  : make_uint2(0u, 0u);
+    }
+    v_absmax<kN>(v, m);
+    const float2 rot1[1] = {rot};
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+      if (h0 + e >= a.Hkv) break;
+      // row index t & 7 selects the chunk swizzle; the row itself starts at dst
+      const long long dst = (static_cast<long long>(b) * a.Hkv + h0 + e) * a.Tp + t;
+      store_k_rows<1>(a.kr + (dst - (t & 7)) * kRowBytes, t & 7, x[e], lane, w_lo, w_hi, w_rest,
+                      rot1, a.eps);
+      const float ex = scale_exp(m[e]);
+      store_v_row(a.vr + (dst - (t & 7)) * kRowBytes, t & 7, v[e], lane, pow2i(ex));
+      if (lane == 0) a.va[dst] = ex;
+    }
   }
+}
+
+// One warp per 16 tokens of a query head, four rows at a time and four dims per
+// lane: q' and dA as operand rows, dg, and the rows' lse and exponent b.  Bound by
+// memory: 1 KiB read and 768 bytes written per row.
+__global__ void __launch_bounds__(256) sink_bwd_rows_kernel(const SinkBwdArgs a) {
+  // operand rows are put together here and leave in 16-byte pieces
+  __shared__ __align__(16) uint8_t stage[8][2][8 * kRowBytes];
+  pdl_start();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, P = a.half_rot;
+  const long long gw = static_cast<long long>(blockIdx.x) * 8 + warp;
+  // heads of one token group are neighbours: their rows lie next to each other
+  const long long grp = gw / a.Hq;
+  const int hq = static_cast<int>(gw - grp * a.Hq);
+  const int per = a.Tp >> 4, b = static_cast<int>(grp / per);
+  if (b >= a.B) return;
+  const int t0 = static_cast<int>(grp - static_cast<long long>(b) * per) * 16;
+  const float icq = 1.0f / pow2_ceil(warp_absmax(a.wq, lane));
+  const int dlo = lane < kMaxPairs ? pair_lo(lane, P) : 0;
+  const int dhi = lane < kMaxPairs ? pair_hi(lane, P) : 0;
+  const float w_lo = __ldg(a.wq + dlo) * icq, w_hi = __ldg(a.wq + dhi) * icq;
+  float4 w_rest = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (lane < 20) {
+    const float4 w = __ldg(reinterpret_cast<const float4*>(a.wq + kRopeDims + 4 * lane));
+    w_rest = make_float4(w.x * icq, w.y * icq, w.z * icq, w.w * icq);
+  }
+  const long long out = (static_cast<long long>(b) * a.Hq + hq) * a.Tp + t0;
+  float bm = kNoScale;
+  constexpr int kN = 4;
+#pragma unroll 1
+  for (int i = 0; i < 16; i += kN) {
+    KRow x[kN];
+    uint2 g2[kN], d2[kN], o2[kN];
+    float2 rot[kN];
+    float l2[kN];
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+      const int t = t0 + i + e;
+      const bool real = t < a.T;
+      const long long at = ((static_cast<long long>(b) * a.T + t) * a.Hq + hq) * kHeadDim;
+      x[e] = load_k_row(real ? a.q + at : nullptr, lane, dlo, dhi);
+      g2[e] = d2[e] = o2[e] = make_uint2(0u, 0u);
+      l2[e] = 0.f;
+      if (real) {
+        g2[e] = __ldg(reinterpret_cast<const uint2*>(a.g + at + 4 * lane));
+        d2[e] = __ldg(reinterpret_cast<const uint2*>(a.dO + at + 4 * lane));
+        o2[e] = __ldg(reinterpret_cast<const uint2*>(a.o + at + 4 * lane));
+        l2[e] = __ldg(a.lse + (static_cast<long long>(b) * a.Hq + hq) * a.T + t) *
+                1.4426950408889634f;
+      }
+      rot[e] = lane < kMaxPairs ? __ldg(a.rot + static_cast<long long>(t) * kMaxPairs + lane)
+                                : make_float2(1.f, 0.f);
+    }
+    float2 u0[kN], u1[kN];
+    float m[kN];
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+      float2 n0, n1;
+      const float2 s0 = sigmoid_both(make_float2(bf16_lo(g2[e].x), bf16_hi(g2[e].x)), &n0);
+      const float2 s1 = sigmoid_both(make_float2(bf16_lo(g2[e].y), bf16_hi(g2[e].y)), &n1);
+      const float2 d0 = make_float2(bf16_lo(d2[e].x), bf16_hi(d2[e].x));
+      const float2 d1 = make_float2(bf16_lo(d2[e].y), bf16_hi(d2[e].y));
+      const float2 q0 = make_float2(bf16_lo(o2[e].x), bf16_hi(o2[e].x));
+      const float2 q1 = make_float2(bf16_lo(o2[e].y), bf16_hi(o2[e].y));
+      u0[e] = __fmul2_rn(d0, s0);
+      u1[e] = __fmul2_rn(d1, s1);
+      const float2 y0 = __fmul2_rn(__fmul2_rn(d0, q0), n0), y1 = __fmul2_rn(__fmul2_rn(d1, q1), n1);
+      const int t = t0 + i + e;
+      if (t < a.T)
+        *reinterpret_cast<uint2*>(
+            a.dg + ((static_cast<long long>(b) * a.T + t) * a.Hq + hq) * kHeadDim + 4 * lane) =
+            make_uint2(pack_bf16x2(y0.x, y0.y), pack_bf16x2(y1.x, y1.y));
+      const float mx = fmaxf(fmaxf(fabsf(u0[e].x), fabsf(u0[e].y)),
+                             fmaxf(fabsf(u1[e].x), fabsf(u1[e].y)));
+      // magnitudes order as their bits do
+      m[e] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+    }
+    store_k_rows<kN>(stage[warp][0], i & 7, x, lane, w_lo, w_hi, w_rest, rot, a.eps);
+    const int md = lane >> 3, c = (lane & 7) >> 1, q = 2 * (lane & 1);
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+      const float be = scale_exp(m[e]), f = pow2i(be);
+      bm = fminf(bm, be);
+      const int r = (i & 7) + e;
+      *reinterpret_cast<uint32_t*>(stage[warp][1] + row_off(r, 4 * md + q) + 4 * c) =
+          pack_f16x2(u0[e].x * f, u0[e].y * f);
+      *reinterpret_cast<uint32_t*>(stage[warp][1] + row_off(r, 4 * md + q + 1) + 4 * c) =
+          pack_f16x2(u1[e].x * f, u1[e].y * f);
+      if (lane == 0) a.row[out + i + e] = make_float4(l2[e], 0.f, be, 0.f);
+    }
+    __syncwarp();
+    const int at = (i & 7) * kRowBytes + 16 * lane;
+#pragma unroll
+    for (int y = 0; y < kN * kRowBytes / 512; ++y) {
+      *reinterpret_cast<uint4*>(a.qr + (out + i - (i & 7)) * kRowBytes + at + 512 * y) =
+          *reinterpret_cast<const uint4*>(stage[warp][0] + at + 512 * y);
+      *reinterpret_cast<uint4*>(a.dr + (out + i - (i & 7)) * kRowBytes + at + 512 * y) =
+          *reinterpret_cast<const uint4*>(stage[warp][1] + at + 512 * y);
+    }
+    // the next four rows use the other half of the stage
+  }
+  if (lane == 0) a.bmin[out >> 4] = bm;
 }
 
 // ------------------------------------------- back through RoPE and the norm
 
-// The raw row of x that a fragment's thread c covers: pairs 8 kk + 2 c + e and
-// dims 48 + 4 c .., 64 + 8 c .., 96 + 8 c ...
-struct RawRow {
-  float lo[6], hi[6], rest[20];
-};
-__device__ __forceinline__ void load_raw(RawRow& x, const uint16_t* row, int c, int P) {
-  if (row == nullptr) {
+// The rotated dims of a warp's 16 rows pass through shared memory (rows of 96
+// bytes), because a fragment's thread holds them two bytes at a time: 16-byte
+// accesses to global memory on one side, 2-byte ones to shared memory on the other.
+constexpr int kRopeRow = kRopeDims * 2;
+constexpr int kRopeBytes = 16 * kRopeRow;
+
+// Start the copy of dims 0 .. 47 of rows 0 .. rows - 1 (row x at src + x * stride)
+// into the warp's buffer; rows past them become zeros.
+__device__ __forceinline__ void rope_fetch(uint8_t* buf, const uint16_t* src, long long stride,
+                                           int rows, int lane) {
 #pragma unroll
-    for (int i = 0; i < 6; ++i) x.lo[i] = x.hi[i] = 0.f;
-#pragma unroll
-    for (int i = 0; i < 20; ++i) x.rest[i] = 0.f;
-    return;
+  for (int i = 0; i < 3; ++i) {
+    const int x = lane + 32 * i, row = x / 6, ch = x - 6 * row;
+    cp_async16(smem_u32(buf) + row * kRopeRow + 16 * ch,
+               src + (row < rows ? row * stride : 0) + 8 * ch, row < rows);
   }
-#pragma unroll
-  for (int i = 0; i < 6; ++i) {
-    const int j = 8 * (i >> 1) + 2 * c + (i & 1);
-    x.lo[i] = bf16_f32(__ldg(row + pair_lo(j, P)));
-    x.hi[i] = bf16_f32(__ldg(row + pair_hi(j, P)));
-  }
-  const uint2 r3 = __ldg(reinterpret_cast<const uint2*>(row + 48 + 4 * c));
-  const uint4 r4 = __ldg(reinterpret_cast<const uint4*>(row + 64 + 8 * c));
-  const uint4 r6 = __ldg(reinterpret_cast<const uint4*>(row + 96 + 8 * c));
-  const uint32_t w[10] = {r3.x, r3.y, r4.x, r4.y, r4.z, r4.w, r6.x, r6.y, r6.z, r6.w};
-#pragma unroll
-  for (int i = 0; i < 10; ++i) {
-    x.rest[2 * i] = bf16_lo(w[i]);
-    x.rest[2 * i + 1] = bf16_hi(w[i]);
-  }
-}
-// Dim of rest[i] (thread c), and its weight.
-__device__ __forceinline__ int rest_dim(int i, int c) {
-  return i < 4 ? 48 + 4 * c + i : (i < 12 ? 64 + 8 * c + (i - 4) : 96 + 8 * c + (i - 12));
-}
-__device__ __forceinline__ float raw_rinv(const RawRow& x, float eps) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < 6; ++i) s += x.lo[i] * x.lo[i] + x.hi[i] * x.hi[i];
-#pragma unroll
-  for (int i = 0; i < 20; ++i) s += x.rest[i] * x.rest[i];
-  s += __shfl_xor_sync(0xffffffffu, s, 1);
-  s += __shfl_xor_sync(0xffffffffu, s, 2);
-  return rsqrtf(s * (1.0f / kHeadDim) + eps);
+  cp_async_commit();
 }
 
-// dx of the two rows (r, r + 8) of a fragment whose accumulators hold dx' in rope
-// order times a factor undone by `f`; dw gets the rows' share by dim (one warp's
-// own shared array).  A null row writes nothing.
+// dx of a fragment's 16 rows whose accumulators hold dx' in rope order times a
+// factor that f undoes for the thread's rows r and r + 8.  src, dst: row 0 of x and
+// dx; rot: the rows' rotations, row 0 of the table.  rope_fetch has been called
+// for the same rows.  dw[d] gains the rows' share of the weight gradient (one
+// warp's own array).
 __device__ __forceinline__ void norm_rope_back(const float (&acc)[16][4], const float (&f)[2],
-                                               const uint16_t* const (&src)[2],
-                                               uint16_t* const (&dst)[2],
-                                               const float2* const (&rot)[2], const float* w,
-                                               float* dw, int lane, int P, float eps) {
-  const int c = lane & 3;
-  float dwl[6], dwh[6], dwr[20];
+                                               uint8_t* buf, const uint16_t* src, uint16_t* dst,
+                                               long long stride, int rows, const float2* rot,
+                                               const float* w, float* dw, int lane, int P,
+                                               float eps) {
+  const int c = lane & 3, r = lane >> 2;
+  float dws[32];  // by i: 0..5 first and 6..11 second dims of the pairs, then the rest
 #pragma unroll
-  for (int i = 0; i < 6; ++i) dwl[i] = dwh[i] = 0.f;
-#pragma unroll
-  for (int i = 0; i < 20; ++i) dwr[i] = 0.f;
+  for (int i = 0; i < 32; ++i) dws[i] = 0.f;
+  uint32_t rest[2][10];
 #pragma unroll
   for (int rr = 0; rr < 2; ++rr) {
+    const int row = r + 8 * rr;
+    uint2 r3 = make_uint2(0u, 0u);
+    uint4 r4 = make_uint4(0u, 0u, 0u, 0u), r6 = r4;
+    if (row < rows) {
+      const uint16_t* p = src + row * stride;
+      r3 = __ldg(reinterpret_cast<const uint2*>(p + 48 + 4 * c));
+      r4 = __ldg(reinterpret_cast<const uint4*>(p + 64 + 8 * c));
+      r6 = __ldg(reinterpret_cast<const uint4*>(p + 96 + 8 * c));
+    }
+    const uint32_t x[10] = {r3.x, r3.y, r4.x, r4.y, r4.z, r4.w, r6.x, r6.y, r6.z, r6.w};
+#pragma unroll
+    for (int i = 0; i < 10; ++i) rest[rr][i] = x[i];
+  }
+  cp_async_wait<0>();
+  __syncwarp();
+#pragma unroll
+  for (int rr = 0; rr < 2; ++rr) {
+    const int row = r + 8 * rr;
+    uint16_t* rp = reinterpret_cast<uint16_t*>(buf + row * kRopeRow);
     RawRow x;
-    load_raw(x, src[rr], c, P);
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+      const int j = 8 * (i >> 1) + 2 * c + (i & 1);
+      x.lo[i] = bf16_f32(rp[pair_lo(j, P)]);
+      x.hi[i] = bf16_f32(rp[pair_hi(j, P)]);
+    }
+#pragma unroll
+    for (int i = 0; i < 10; ++i) {
+      x.rest[2 * i] = bf16_lo(rest[rr][i]);
+      x.rest[2 * i + 1] = bf16_hi(rest[rr][i]);
+    }
     const float rinv = raw_rinv(x, eps);
     float dot = 0.f;
     float yl[6], yh[6], yr[20];
 #pragma unroll
     for (int i = 0; i < 6; ++i) {
       const int j = 8 * (i >> 1) + 2 * c + (i & 1);
-      const float2 cs = rot[rr] != nullptr ? __ldg(rot[rr] + j) : make_float2(1.f, 0.f);
+      const float2 cs = __ldg(rot + row * kMaxPairs + j);
       const float u = acc[2 * (i >> 1)][2 * rr + (i & 1)] * f[rr];
       const float v = acc[2 * (i >> 1) + 1][2 * rr + (i & 1)] * f[rr];
       const float al = u * cs.x + v * cs.y, ah = v * cs.x - u * cs.y;
       x.lo[i] *= rinv;
       x.hi[i] *= rinv;
-      dwl[i] += al * x.lo[i];
-      dwh[i] += ah * x.hi[i];
+      dws[i] += al * x.lo[i];
+      dws[6 + i] += ah * x.hi[i];
       yl[i] = al * __ldg(w + pair_lo(j, P));
       yh[i] = ah * __ldg(w + pair_hi(j, P));
       dot += yl[i] * x.lo[i] + yh[i] * x.hi[i];
     }
 #pragma unroll
-    for (int i = 0; i < 20; ++i) {
-      const float al = acc[6 + (i >> 1)][2 * rr + (i & 1)] * f[rr];
-      x.rest[i] *= rinv;
-      dwr[i] += al * x.rest[i];
-      yr[i] = al * __ldg(w + rest_dim(i, c));
-      dot += yr[i] * x.rest[i];
+    for (int i = 0; i < 10; ++i) {
+      const float2 ww = __ldg(reinterpret_cast<const float2*>(w + rest_dim(2 * i, c)));
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int k = 2 * i + e;
+        const float al = acc[6 + i][2 * rr + e] * f[rr];
+        x.rest[k] *= rinv;
+        dws[12 + k] += al * x.rest[k];
+        yr[k] = al * (e ? ww.y : ww.x);
+        dot += yr[k] * x.rest[k];
+      }
     }
     dot += __shfl_xor_sync(0xffffffffu, dot, 1);
     dot += __shfl_xor_sync(0xffffffffu, dot, 2);
     const float mean = dot * (1.0f / kHeadDim);
-    if (dst[rr] != nullptr) {
 #pragma unroll
-      for (int i = 0; i < 6; ++i) {
-        const int j = 8 * (i >> 1) + 2 * c + (i & 1);
-        *reinterpret_cast<__nv_bfloat16*>(dst[rr] + pair_lo(j, P)) =
-            __float2bfloat16_rn(rinv * (yl[i] - x.lo[i] * mean));
-        *reinterpret_cast<__nv_bfloat16*>(dst[rr] + pair_hi(j, P)) =
-            __float2bfloat16_rn(rinv * (yh[i] - x.hi[i] * mean));
-      }
+    for (int i = 0; i < 6; ++i) {
+      const int j = 8 * (i >> 1) + 2 * c + (i & 1);
+      const uint32_t y = pack_bf16x2(rinv * (yl[i] - x.lo[i] * mean),
+                                     rinv * (yh[i] - x.hi[i] * mean));
+      rp[pair_lo(j, P)] = static_cast<uint16_t>(y);
+      rp[pair_hi(j, P)] = static_cast<uint16_t>(y >> 16);
+    }
+    if (row < rows) {
       uint32_t o[10];
 #pragma unroll
       for (int i = 0; i < 10; ++i)
         o[i] = pack_bf16x2(rinv * (yr[2 * i] - x.rest[2 * i] * mean),
                            rinv * (yr[2 * i + 1] - x.rest[2 * i + 1] * mean));
-      *reinterpret_cast<uint2*>(dst[rr] + 48 + 4 * c) = make_uint2(o[0], o[1]);
-      *reinterpret_cast<uint4*>(dst[rr] + 64 + 8 * c) = make_uint4(o[2], o[3], o[4], o[5]);
-      *reinterpret_cast<uint4*>(dst[rr] + 96 + 8 * c) = make_uint4(o[6], o[7], o[8], o[9]);
+      uint16_t* p = dst + row * stride;
+      *reinterpret_cast<uint2*>(p + 48 + 4 * c) = make_uint2(o[0], o[1]);
+      *reinterpret_cast<uint4*>(p + 64 + 8 * c) = make_uint4(o[2], o[3], o[4], o[5]);
+      *reinterpret_cast<uint4*>(p + 96 + 8 * c) = make_uint4(o[6], o[7], o[8], o[9]);
     }
   }
-  // sums over the fragment's rows: lanes of one c
-  auto add = [&](float x, int d) {
-    x += __shfl_xor_sync(0xffffffffu, x, 4);
-    x += __shfl_xor_sync(0xffffffffu, x, 8);
-    x += __shfl_xor_sync(0xffffffffu, x, 16);
-    if (lane < 4) dw[d] += x;
-  };
+  __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 6; ++i) {
-    const int j = 8 * (i >> 1) + 2 * c + (i & 1);
-    add(dwl[i], pair_lo(j, P));
-    add(dwh[i], pair_hi(j, P));
+  for (int i = 0; i < 3; ++i) {
+    const int x = lane + 32 * i, row = x / 6, ch = x - 6 * row;
+    if (row < rows)
+      *reinterpret_cast<uint4*>(dst + row * stride + 8 * ch) =
+          *reinterpret_cast<const uint4*>(buf + row * kRopeRow + 16 * ch);
   }
+  __syncwarp();  // the buffer may take the next rows
+  // Sums over the fragment's rows: the eight lanes of one c each end up with four
+  // of the 32 values (a lane hands over the half that its partner keeps).
+  float h16[16], h8[8], h4[4];
+  const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
 #pragma unroll
-  for (int i = 0; i < 20; ++i) add(dwr[i], rest_dim(i, c));
+  for (int i = 0; i < 16; ++i)
+    h16[i] = (b4 ? dws[16 + i] : dws[i]) +
+             __shfl_xor_sync(0xffffffffu, b4 ? dws[i] : dws[16 + i], 16);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    h8[i] = (b3 ? h16[8 + i] : h16[i]) +
+            __shfl_xor_sync(0xffffffffu, b3 ? h16[i] : h16[8 + i], 8);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    h4[i] = (b2 ? h8[4 + i] : h8[i]) + __shfl_xor_sync(0xffffffffu, b2 ? h8[i] : h8[4 + i], 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int k = (b4 ? 16 : 0) + (b3 ? 8 : 0) + (b2 ? 4 : 0) + i;
+    const int p = k < 6 ? k : k - 6, j = 8 * (p >> 1) + 2 * c + (p & 1);
+    const int d = k < 6 ? pair_lo(j, P) : (k < 12 ? pair_hi(j, P) : rest_dim(k - 12, c));
+    dw[d] += h4[i];
+  }
 }
 
 // ---------------------------------------------------------- query-major pass
@@ -277,9 +394,12 @@ struct alignas(1024) QSmem {
   uint8_t ks[kSinkBytes], vs[kSinkBytes];
   float vf[kBand + kMaxSink];  // 2^(amin - a) of each key row
   float dw[4][kHeadDim];
+  uint8_t rope[4][kRopeBytes];
   uint64_t full;
   int abort;
 };
+
+static_assert(sizeof(QSmem) <= 115712, "two CTAs per SM");
 
 enum BwdSite { kSiteBQ = 0xF0, kSiteBFull, kSiteBEmpty, kSiteBTile };
 
@@ -329,7 +449,7 @@ __global__ void __launch_bounds__(kQThreads, 2) sink_bwd_q_kernel(const SinkBwdA
   }
   if (tid == 0) a.amin[chain * a.tiles + tile] = am;
   const float cq = pow2_ceil(warp_absmax(a.wq, lane)), ck = pow2_ceil(warp_absmax(a.wk, lane));
-  const float icq = 1.0f / cq, sc = a.scale_log2 * cq * ck;
+  const float sc = a.scale_log2 * cq * ck;
   volatile int* abort = &sm.abort;
   __syncthreads();
   const bool ok = __all_sync(0xffffffffu, mbar_wait(&sm.full, 0, abort, a.err, kSiteBFull));
@@ -342,178 +462,134 @@ __global__ void __launch_bounds__(kQThreads, 2) sink_bwd_q_kernel(const SinkBwdA
   const int i0 = t0 + 16 * w;
   const int lo = max(0, 8 - (i0 >> 4));
   const bool sink = a.n_sink > 0 && i0 >= kWindow;
-  const float2* rot[2];
-  bool real[2];
-#pragma unroll
-  for (int rr = 0; rr < 2; ++rr) {
-    const int t = i0 + r + 8 * rr;
-    real[rr] = t < a.T;
-    rot[rr] = a.rot + static_cast<long long>(t) * kMaxPairs;
-  }
+  const long long stride = static_cast<long long>(a.Hq) * kHeadDim;
+  const int rows = min(16, a.T - i0);  // none or fewer past the sequence's end
 #pragma unroll 1
   for (int h = 0; h < a.G; ++h) {
     const int hq = kvh * a.G + h;
-    const long long hrow = (static_cast<long long>(b) * a.Hq + hq) * a.Tp;
+    const long long hrow = (static_cast<long long>(b) * a.Hq + hq) * a.Tp + i0;
+    // ---- q' and dA as A fragments: words c of the rows' chunks
     uint32_t qf[8][4], df[8][4];
-    float L2[2], Dn[2], fs[2], bexp[2];
-    const uint16_t* qsrc[2];
-    uint16_t* qdst[2];
+    float L2[2], fs[2], Dn[2];
+    const long long raw = ((static_cast<long long>(b) * a.T + min(i0, a.T - 1)) * a.Hq + hq) *
+                          kHeadDim;
+    rope_fetch(sm.rope[w], a.q + raw, stride, rows, lane);
 #pragma unroll
     for (int rr = 0; rr < 2; ++rr) {
-      const int t = i0 + r + 8 * rr;
-      const long long at = ((static_cast<long long>(b) * a.T + t) * a.Hq + hq) * kHeadDim;
-      qsrc[rr] = real[rr] ? a.q + at : nullptr;
-      qdst[rr] = real[rr] ? a.dq + at : nullptr;
-      // ---- q'
-      {
-        RawRow x;
-        load_raw(x, qsrc[rr], c, P);
-        const float rinv = raw_rinv(x, a.eps) * icq;
-#pragma unroll
-        for (int kk = 0; kk < 3; ++kk) {
-          float ul[2], uh[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int j = 8 * kk + 2 * c + e;
-            const float2 cs = __ldg(rot[rr] + j);
-            const float u = x.lo[2 * kk + e] * rinv * __ldg(a.wq + pair_lo(j, P));
-            const float v = x.hi[2 * kk + e] * rinv * __ldg(a.wq + pair_hi(j, P));
-            ul[e] = u * cs.x - v * cs.y;
-            uh[e] = v * cs.x + u * cs.y;
-          }
-          qf[kk][rr] = pack_f16x2(ul[0], ul[1]);
-          qf[kk][2 + rr] = pack_f16x2(uh[0], uh[1]);
-        }
-#pragma unroll
-        for (int i = 0; i < 10; ++i)
-          qf[3 + (i >> 1)][2 * (i & 1) + rr] =
-              pack_f16x2(x.rest[2 * i] * rinv * __ldg(a.wq + rest_dim(2 * i, c)),
-                         x.rest[2 * i + 1] * rinv * __ldg(a.wq + rest_dim(2 * i + 1, c)));
-      }
-      // ---- dg, dA, D
-      {
-        float da[32];
-        float D = 0.f, m = 0.f;
-#pragma unroll
-        for (int md = 0; md < 4; ++md) {
-          uint4 g4 = make_uint4(0u, 0u, 0u, 0u), d4 = g4, o4 = g4;
-          if (real[rr]) {
-            g4 = __ldg(reinterpret_cast<const uint4*>(a.g + at + 32 * md + 8 * c));
-            d4 = __ldg(reinterpret_cast<const uint4*>(a.dO + at + 32 * md + 8 * c));
-            o4 = __ldg(reinterpret_cast<const uint4*>(a.o + at + 32 * md + 8 * c));
-          }
-          const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w}, dw4[4] = {d4.x, d4.y, d4.z, d4.w},
-                         ow[4] = {o4.x, o4.y, o4.z, o4.w};
-          uint32_t y[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float2 gx = make_float2(bf16_lo(gw[x]), bf16_hi(gw[x]));
-            const float2 dx = make_float2(bf16_lo(dw4[x]), bf16_hi(dw4[x]));
-            const float2 ox = make_float2(bf16_lo(ow[x]), bf16_hi(ow[x]));
-            const float2 s = sigmoid2(gx), n = sigmoid2(make_float2(-gx.x, -gx.y));
-            const float2 p = __fmul2_rn(dx, ox), t2 = __fmul2_rn(p, n), u = __fmul2_rn(dx, s);
-            D += p.x + p.y;
-            y[x] = pack_bf16x2(t2.x, t2.y);
-            da[8 * md + 2 * x] = u.x;
-            da[8 * md + 2 * x + 1] = u.y;
-            m = fmaxf(m, fmaxf(fabsf(u.x), fabsf(u.y)));
-          }
-          if (real[rr])
-            *reinterpret_cast<uint4*>(a.dg + at + 32 * md + 8 * c) =
-                make_uint4(y[0], y[1], y[2], y[3]);
-        }
-        D += __shfl_xor_sync(0xffffffffu, D, 1);
-        D += __shfl_xor_sync(0xffffffffu, D, 2);
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const float be = scale_exp(m), f = pow2i(be);
-#pragma unroll
-        for (int md = 0; md < 4; ++md)
-#pragma unroll
-          for (int x = 0; x < 4; ++x)  // word x of the group: k-step 2 md + x / 2, half x & 1
-            df[2 * md + (x >> 1)][2 * (x & 1) + rr] =
-                pack_f16x2(da[8 * md + 2 * x] * f, da[8 * md + 2 * x + 1] * f);
-        const float l2 =
-            real[rr] ? __ldg(a.lse + (static_cast<long long>(b) * a.Hq + hq) * a.T + t) *
-                           1.4426950408889634f
-                     : 0.0f;
-        bexp[rr] = be;
-        L2[rr] = l2;
-        const float Db = D * f;
-        Dn[rr] = Db * pow2i(am);
-        fs[rr] = scale2(a.scale * ck, -(be + am));
-        if (c == 0) a.row[hrow + t] = make_float4(l2, Db, be, 0.f);
-      }
-      // ---- the operand rows of the key-major passes
-      uint8_t* qrow = a.qr + (hrow + t - (t & 7)) * kRowBytes;
-      uint8_t* drow = a.dr + (hrow + t - (t & 7)) * kRowBytes;
+      const uint8_t* qrow = a.qr + hrow * kRowBytes + 4 * c;
+      const uint8_t* drow = a.dr + hrow * kRowBytes + 4 * c;
+      const float4 rec = __ldg(a.row + hrow + r + 8 * rr);
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          *reinterpret_cast<uint32_t*>(qrow + row_off(t & 7, 2 * kk + hf) + 4 * c) =
-              qf[kk][2 * hf + rr];
-          *reinterpret_cast<uint32_t*>(drow + row_off(t & 7, 2 * kk + hf) + 4 * c) =
-              df[kk][2 * hf + rr];
+          qf[kk][2 * hf + rr] =
+              __ldg(reinterpret_cast<const uint32_t*>(qrow + row_off(r + 8 * rr, 2 * kk + hf)));
+          df[kk][2 * hf + rr] =
+              __ldg(reinterpret_cast<const uint32_t*>(drow + row_off(r + 8 * rr, 2 * kk + hf)));
         }
+      L2[rr] = rec.x;
+      fs[rr] = scale2(a.scale * ck, -(rec.z + am));
     }
+    // the next head's rows, and this one's raw q for the end, towards L2
     {
-      float bm = fminf(bexp[0], bexp[1]);
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) bm = fminf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
-      if (lane == 0) a.bmin[(hrow + i0) >> 4] = bm;
+      const long long nx = hrow * kRowBytes + (h + 1 < a.G ? static_cast<long long>(a.Tp) * kRowBytes : 0);
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.qr + nx + 128 * lane));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.dr + nx + 128 * lane));
+      const int t = min(i0 + (lane >> 1), a.T - 1);
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(
+          a.q + ((static_cast<long long>(b) * a.T + t) * a.Hq + hq) * kHeadDim + 64 * (lane & 1)));
     }
-    // ---- the blocks: S, dP, dS, dQ
+    // ---- S and dP of all blocks; P and dP stay in registers (fp16) until D, the
+    // sum of their products, is known
+    uint32_t pf[10][4], gf[10][4];
+    Dn[0] = Dn[1] = 0.f;
+#pragma unroll
+    for (int x = 0; x < 10; ++x) {
+      if (x == 9 ? sink : x >= lo) {
+        const uint32_t kt = x == 9 ? smem_u32(sm.ks) : smem_u32(sm.k) + 16 * (w + x) * kRowBytes;
+        const uint32_t vt = x == 9 ? smem_u32(sm.vs) : smem_u32(sm.v) + 16 * (w + x) * kRowBytes;
+        const float* vf = x == 9 ? sm.vf + kBand : sm.vf + 16 * (w + x);
+        float s[2][4], dp[2][4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+          dp[n][0] = dp[n][1] = dp[n][2] = dp[n][3] = 0.f;
+        }
+        uint32_t kf[2][4], vg[2][4];
+        ldsm_x4(kt + k_lane, kf[0]);
+        ldsm_x4(vt + k_lane, vg[0]);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          if (kk < 7) {
+            ldsm_x4((kt + k_lane) ^ ((kk + 1) << 5), kf[(kk + 1) & 1]);
+            ldsm_x4((vt + k_lane) ^ ((kk + 1) << 5), vg[(kk + 1) & 1]);
+          }
+          mma_f16(s[0], qf[kk], kf[kk & 1][0], kf[kk & 1][1]);
+          mma_f16(s[1], qf[kk], kf[kk & 1][2], kf[kk & 1][3]);
+          mma_f16(dp[0], df[kk], vg[kk & 1][0], vg[kk & 1][1]);
+          mma_f16(dp[1], df[kk], vg[kk & 1][2], vg[kk & 1][3]);
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float2 f2 = *reinterpret_cast<const float2*>(vf + 8 * n + 2 * c);
+          float p[4], y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int rr = e >> 1, row = r + 8 * rr, col = 8 * n + 2 * c + (e & 1);
+            p[e] = ex2_approx(fmaf(s[n][e], sc, -L2[rr]));
+            y[e] = dp[n][e] * ((e & 1) ? f2.y : f2.x);
+            bool hide = false;
+            if (x == 0) hide = col <= row;
+            if (x == 8) hide = col > row;
+            if (x == 9) hide = col >= a.n_sink || col > i0 + row - kWindow;
+            if (hide) p[e] = y[e] = 0.f;
+          }
+          pf[x][2 * n] = pack_f16x2(p[0], p[1]);
+          pf[x][2 * n + 1] = pack_f16x2(p[2], p[3]);
+          gf[x][2 * n] = pack_f16x2(y[0], y[1]);
+          gf[x][2 * n + 1] = pack_f16x2(y[2], y[3]);
+          Dn[0] += p[0] * y[0] + p[1] * y[1];
+          Dn[1] += p[2] * y[2] + p[3] * y[3];
+        }
+      } else {
+        pf[x][0] = pf[x][1] = pf[x][2] = pf[x][3] = 0u;
+        gf[x][0] = gf[x][1] = gf[x][2] = gf[x][3] = 0u;
+      }
+    }
+#pragma unroll
+    for (int rr = 0; rr < 2; ++rr) {
+      Dn[rr] += __shfl_xor_sync(0xffffffffu, Dn[rr], 1);
+      Dn[rr] += __shfl_xor_sync(0xffffffffu, Dn[rr], 2);
+      if (c == 0)
+        reinterpret_cast<float*>(a.row + hrow + r + 8 * rr)[1] = Dn[rr] * pow2i(-am);
+    }
+    // ---- dQ = dS K', dS = P (dP - D)
     float dq[16][4];
 #pragma unroll
     for (int n = 0; n < 16; ++n) dq[n][0] = dq[n][1] = dq[n][2] = dq[n][3] = 0.f;
-#pragma unroll 1
-    for (int x = lo; x < (sink ? 10 : 9); ++x) {
+#pragma unroll
+    for (int x = 0; x < 10; ++x) {
+      if (!(x == 9 ? sink : x >= lo)) continue;
       const uint32_t kt = x == 9 ? smem_u32(sm.ks) : smem_u32(sm.k) + 16 * (w + x) * kRowBytes;
-      const uint32_t vt = x == 9 ? smem_u32(sm.vs) : smem_u32(sm.v) + 16 * (w + x) * kRowBytes;
-      const float* vf = x == 9 ? sm.vf + kBand : sm.vf + 16 * (w + x);
-      float s[2][4], dp[2][4];
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-        dp[n][0] = dp[n][1] = dp[n][2] = dp[n][3] = 0.f;
-      }
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        uint32_t kf[4], vg[4];
-        ldsm_x4((kt + k_lane) ^ (kk << 5), kf);
-        ldsm_x4((vt + k_lane) ^ (kk << 5), vg);
-        mma_f16(s[0], qf[kk], kf[0], kf[1]);
-        mma_f16(s[1], qf[kk], kf[2], kf[3]);
-        mma_f16(dp[0], df[kk], vg[0], vg[1]);
-        mma_f16(dp[1], df[kk], vg[2], vg[3]);
-      }
       uint32_t ds[4];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const float2 f2 = *reinterpret_cast<const float2*>(vf + 8 * n + 2 * c);
-        float y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int rr = e >> 1, row = r + 8 * rr, col = 8 * n + 2 * c + (e & 1);
-          const float p = ex2_approx(fmaf(s[n][e], sc, -L2[rr]));
-          y[e] = p * fmaf(dp[n][e], (e & 1) ? f2.y : f2.x, -Dn[rr]);
-          if (x == 0 && col <= row) y[e] = 0.f;
-          if (x == 8 && col > row) y[e] = 0.f;
-          if (x == 9 && (col >= a.n_sink || col > i0 + row - kWindow)) y[e] = 0.f;
-        }
-        ds[2 * n] = pack_f16x2(y[0], y[1]);
-        ds[2 * n + 1] = pack_f16x2(y[2], y[3]);
+      for (int i = 0; i < 4; ++i) {
+        const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&pf[x][i]));
+        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&gf[x][i]));
+        ds[i] = pack_f16x2(p.x * (y.x - Dn[i & 1]), p.y * (y.y - Dn[i & 1]));
       }
+      uint32_t kf[2][4];
+      ldsm_x4_trans(kt + t_lane, kf[0]);
 #pragma unroll
       for (int nd = 0; nd < 16; nd += 2) {
-        uint32_t kf[4];
-        ldsm_x4_trans((kt + t_lane) ^ (nd << 4), kf);
-        mma_f16(dq[nd], ds, kf[0], kf[1]);
-        mma_f16(dq[nd + 1], ds, kf[2], kf[3]);
+        if (nd < 14) ldsm_x4_trans((kt + t_lane) ^ ((nd + 2) << 4), kf[((nd >> 1) + 1) & 1]);
+        mma_f16(dq[nd], ds, kf[(nd >> 1) & 1][0], kf[(nd >> 1) & 1][1]);
+        mma_f16(dq[nd + 1], ds, kf[(nd >> 1) & 1][2], kf[(nd >> 1) & 1][3]);
       }
     }
-    norm_rope_back(dq, fs, qsrc, qdst, rot, a.wq, sm.dw[w], lane, P, a.eps);
+    norm_rope_back(dq, fs, sm.rope[w], a.q + raw, a.dq + raw, stride, rows,
+                   a.rot + static_cast<long long>(i0) * kMaxPairs, a.wq, sm.dw[w], lane, P, a.eps);
   }
   __syncthreads();
   for (int d = tid; d < kHeadDim; d += kQThreads)
@@ -770,6 +846,7 @@ struct alignas(1024) KSmem {
   uint8_t d[kKStages][kStageBytes];
   float4 row[kKStages][kStageRows];
   float dw[4][kHeadDim];
+  uint8_t rope[4][kRopeBytes];
   uint64_t full[kKStages], empty[kKStages], tile;
   int abort;
 };
@@ -885,6 +962,11 @@ __global__ void __launch_bounds__(kKThreads, 2) sink_bwd_k_kernel(const SinkBwdA
       }
     return;
   }
+  const long long raw = ((static_cast<long long>(b) * a.T + min(j0, a.T - 1)) * a.Hkv + kvh) *
+                        kHeadDim;
+  const long long stride = static_cast<long long>(a.Hkv) * kHeadDim;
+  const int rows = min(16, a.T - j0);
+  rope_fetch(sm.rope[w], a.k + raw, stride, rows, lane);
   // ---- true scale; the sinks' sums from the queries beyond the window
   const float fk = scale2(a.scale * cq, -(bm + am)), fv = scale2(1.0f, -bm);
   const bool add = a.n_sink > 0 && tile == 0 && w == 0;
@@ -904,16 +986,10 @@ __global__ void __launch_bounds__(kKThreads, 2) sink_bwd_k_kernel(const SinkBwdA
       dv[n][2 * rr] = fmaf(dv[n][2 * rr], fv, y.x);
       dv[n][2 * rr + 1] = fmaf(dv[n][2 * rr + 1], fv, y.y);
     }
-  const uint16_t* ksrc[2];
-  uint16_t* kdst[2];
-  const float2* rot[2];
 #pragma unroll
   for (int rr = 0; rr < 2; ++rr) {
     const int t = j0 + r + 8 * rr;
     const long long at = ((static_cast<long long>(b) * a.T + t) * a.Hkv + kvh) * kHeadDim;
-    ksrc[rr] = t < a.T ? a.k + at : nullptr;
-    kdst[rr] = t < a.T ? a.dk + at : nullptr;
-    rot[rr] = a.rot + static_cast<long long>(t) * kMaxPairs;
     if (t < a.T)
 #pragma unroll
       for (int m = 0; m < 4; ++m)
@@ -924,29 +1000,31 @@ __global__ void __launch_bounds__(kKThreads, 2) sink_bwd_k_kernel(const SinkBwdA
                        pack_bf16x2(dv[4 * m + 3][2 * rr], dv[4 * m + 3][2 * rr + 1]));
   }
   const float one[2] = {1.0f, 1.0f};
-  norm_rope_back(dk, one, ksrc, kdst, rot, a.wk, sm.dw[w], lane, a.half_rot, a.eps);
+  norm_rope_back(dk, one, sm.rope[w], a.k + raw, a.dk + raw, stride, rows,
+                 a.rot + static_cast<long long>(j0) * kMaxPairs, a.wk, sm.dw[w], lane, a.half_rot,
+                 a.eps);
   __syncthreads();
   for (int d = tid; d < kHeadDim; d += kKThreads)
     a.dwk_part[static_cast<long long>(blockIdx.x) * kHeadDim + d] =
         (sm.dw[0][d] + sm.dw[1][d]) + (sm.dw[2][d] + sm.dw[3][d]);
 }
 
-// dwq (blockIdx.y 0) and dwk (1): 16 dims per block, 16 slices of the CTAs' partial
+// dwq (blockIdx.y 0) and dwk (1): 16 dims per block, 64 slices of the CTAs' partial
 // sums each, then the slices in order.
-__global__ void __launch_bounds__(256) sink_bwd_w_kernel(const SinkBwdArgs a) {
-  __shared__ float part[16][17];
+__global__ void __launch_bounds__(1024) sink_bwd_w_kernel(const SinkBwdArgs a) {
+  __shared__ float part[64][17];
   pdl_start();
   const int d = threadIdx.x & 15, s = threadIdx.x >> 4, dim = 16 * blockIdx.x + d;
   const float* src = blockIdx.y == 0 ? a.dwq_part : a.dwk_part;
   const long long n = static_cast<long long>(a.B) * a.Hkv * a.tiles;
   float x = 0.f;
 #pragma unroll 8
-  for (long long i = s; i < n; i += 16) x += src[i * kHeadDim + dim];
+  for (long long i = s; i < n; i += 64) x += src[i * kHeadDim + dim];
   part[s][d] = x;
   __syncthreads();
   if (s == 0) {
     float y = 0.f;
-    for (int i = 0; i < 16; ++i) y += part[i][d];
+    for (int i = 0; i < 64; ++i) y += part[i][d];
     float* out = blockIdx.y == 0 ? a.dwq : a.dwk;
     out[dim] += y;
   }
@@ -976,10 +1054,13 @@ int launch_sink_bwd(const SinkBwdArgs& a, cudaStream_t stream) {
   const long long tokens = static_cast<long long>(a.B) * a.Tp;
   const long long tiles = static_cast<long long>(a.B) * a.Hkv * a.tiles;
   const long long chains = static_cast<long long>(a.B) * a.Hkv;
-  if (tokens / 8 > 0x7fffffffLL || tiles > 0x7fffffffLL || chains * 16 > 0x7fffffffLL)
+  const long long row_warps = tokens / 16 * a.Hq;
+  if (row_warps / 8 > 0x7fffffffLL || tokens / 8 > 0x7fffffffLL || tiles > 0x7fffffffLL || chains * 16 > 0x7fffffffLL)
     return SWA_ERR_UNSUPPORTED;
   const auto grid = [](long long n) { return static_cast<unsigned>(n); };
   rc = launch_dependent(snk::sink_bwd_kv_kernel, grid((tokens + 7) / 8), 256, 0, stream, a);
+  if (rc == SWA_OK)
+    rc = launch_dependent(snk::sink_bwd_rows_kernel, grid((row_warps + 7) / 8), 256, 0, stream, a);
   if (rc == SWA_OK)
     rc = launch_dependent(snk::sink_bwd_q_kernel, grid(tiles), snk::kQThreads, sizeof(snk::QSmem),
                           stream, a);
@@ -995,7 +1076,7 @@ int launch_sink_bwd(const SinkBwdArgs& a, cudaStream_t stream) {
   if (rc != SWA_OK) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kHeadDim / 16, 2);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(1024);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

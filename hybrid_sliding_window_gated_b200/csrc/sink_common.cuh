@@ -138,43 +138,180 @@ __device__ __forceinline__ void rest_pos(int lane, int* chunk0, int* byte) {
   }
 }
 
-// k' / ck of one row, fp16, in rope order into row r of `tile`; w_* are this
-// lane's weights divided by ck, rot its pair's rotation at the row's position.
-__device__ __forceinline__ void store_k_row(uint8_t* tile, int r, const KRow& x, int lane,
-                                            float w_lo, float w_hi, float4 w_rest, float2 rot,
-                                            float eps) {
-  const float lo = bf16_f32(x.lo), hi = bf16_f32(x.hi);
-  const float a0 = bf16_lo(x.rest.x), a1 = bf16_hi(x.rest.x);
-  const float a2 = bf16_lo(x.rest.y), a3 = bf16_hi(x.rest.y);
-  float ss = lo * lo + hi * hi + a0 * a0 + a1 * a1 + a2 * a2 + a3 * a3;
+// k' / ck of N rows, fp16, in rope order into rows r0 .. of `tile` (row_at(e) is the
+// row e is swizzled as); w_* are this lane's weights divided by ck, rot its pair's
+// rotation at each row's position.  The rows' chains of shuffles run side by side.
+template <int N>
+__device__ __forceinline__ void store_k_rows(uint8_t* tile, int r0, const KRow (&x)[N], int lane,
+                                             float w_lo, float w_hi, float4 w_rest,
+                                             const float2 (&rot)[N], float eps) {
+  float ss[N];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const float rinv = rsqrtf(ss * (1.0f / kHeadDim) + eps);
-  if (lane < kMaxPairs) {
-    const float u = lo * rinv * w_lo, v = hi * rinv * w_hi;
-    const int kk = lane >> 3, m = lane & 7;
-    *reinterpret_cast<__half*>(tile + row_off(r, 2 * kk) + 2 * m) =
-        __float2half_rn(u * rot.x - v * rot.y);
-    *reinterpret_cast<__half*>(tile + row_off(r, 2 * kk + 1) + 2 * m) =
-        __float2half_rn(v * rot.x + u * rot.y);
+  for (int e = 0; e < N; ++e) {
+    const float lo = bf16_f32(x[e].lo), hi = bf16_f32(x[e].hi);
+    const float a0 = bf16_lo(x[e].rest.x), a1 = bf16_hi(x[e].rest.x);
+    const float a2 = bf16_lo(x[e].rest.y), a3 = bf16_hi(x[e].rest.y);
+    ss[e] = lo * lo + hi * hi + a0 * a0 + a1 * a1 + a2 * a2 + a3 * a3;
   }
-  if (lane < 20) {
-    int c0, by;
-    rest_pos(lane, &c0, &by);
-    *reinterpret_cast<uint32_t*>(tile + row_off(r, c0) + by) =
-        pack_f16x2(a0 * rinv * w_rest.x, a1 * rinv * w_rest.y);
-    *reinterpret_cast<uint32_t*>(tile + row_off(r, c0 + 1) + by) =
-        pack_f16x2(a2 * rinv * w_rest.z, a3 * rinv * w_rest.w);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int e = 0; e < N; ++e) ss[e] += __shfl_xor_sync(0xffffffffu, ss[e], o);
+  uint32_t pair[N], r01[N], r23[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const float rinv = rsqrtf(ss[e] * (1.0f / kHeadDim) + eps);
+    const float u = bf16_f32(x[e].lo) * rinv * w_lo, v = bf16_f32(x[e].hi) * rinv * w_hi;
+    pair[e] = pack_f16x2(u * rot[e].x - v * rot[e].y, v * rot[e].x + u * rot[e].y);
+    r01[e] = pack_f16x2(bf16_lo(x[e].rest.x) * rinv * w_rest.x,
+                        bf16_hi(x[e].rest.x) * rinv * w_rest.y);
+    r23[e] = pack_f16x2(bf16_lo(x[e].rest.y) * rinv * w_rest.z,
+                        bf16_hi(x[e].rest.y) * rinv * w_rest.w);
+  }
+  int c0, by;
+  rest_pos(lane, &c0, &by);
+  const int kk = lane >> 3, m = lane & 7;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const int r = r0 + e;
+    if (lane < kMaxPairs) {
+      *reinterpret_cast<uint16_t*>(tile + row_off(r, 2 * kk) + 2 * m) =
+          static_cast<uint16_t>(pair[e]);
+      *reinterpret_cast<uint16_t*>(tile + row_off(r, 2 * kk + 1) + 2 * m) =
+          static_cast<uint16_t>(pair[e] >> 16);
+    }
+    if (lane < 20) {
+      *reinterpret_cast<uint32_t*>(tile + row_off(r, c0) + by) = r01[e];
+      *reinterpret_cast<uint32_t*>(tile + row_off(r, c0 + 1) + by) = r23[e];
+    }
   }
 }
 
-// 16-byte chunk c (dims 8 c .. 8 c + 7) of V row r into split order.
-__device__ __forceinline__ void store_v_chunk(uint8_t* tile, int r, int c, uint4 x) {
-  const int m = c >> 2, by = 4 * (c & 3);
-  *reinterpret_cast<uint32_t*>(tile + row_off(r, 4 * m) + by) = x.x;
-  *reinterpret_cast<uint32_t*>(tile + row_off(r, 4 * m + 1) + by) = x.y;
-  *reinterpret_cast<uint32_t*>(tile + row_off(r, 4 * m + 2) + by) = x.z;
-  *reinterpret_cast<uint32_t*>(tile + row_off(r, 4 * m + 3) + by) = x.w;
+// The largest |v| of N rows whose dims 4 lane .. + 3 this lane holds (bf16 pairs).
+// bf16 magnitudes order as their bit patterns do (an inf or NaN counts as inf).
+template <int N>
+__device__ __forceinline__ void v_absmax(const uint2 (&v)[N], float (&m)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const uint32_t a = __vmaxu2(v[e].x & 0x7fff7fffu, v[e].y & 0x7fff7fffu);
+    const uint32_t top = __reduce_max_sync(0xffffffffu, max(a & 0xffffu, a >> 16));
+    m[e] = __uint_as_float(min(top, 0x7f80u) << 16);
+  }
+}
+// Dims 4 lane .. + 3 of a V row times f, fp16, in split order into row r of `tile`:
+// they are 32 m + 8 c + 2 q .. with q = 0 or 2, words q and q + 1 of the group.
+__device__ __forceinline__ void store_v_row(uint8_t* tile, int r, uint2 v, int lane, float f) {
+  const int m = lane >> 3, c = (lane & 7) >> 1, q = 2 * (lane & 1);
+  *reinterpret_cast<uint32_t*>(tile + row_off(r, 4 * m + q) + 4 * c) =
+      pack_f16x2(bf16_lo(v.x) * f, bf16_hi(v.x) * f);
+  *reinterpret_cast<uint32_t*>(tile + row_off(r, 4 * m + q + 1) + 4 * c) =
+      pack_f16x2(bf16_lo(v.y) * f, bf16_hi(v.y) * f);
+}
+
+// 2^x for a whole x in [-126, 127]
+__device__ __forceinline__ float pow2i(float x) {
+  return __uint_as_float(static_cast<uint32_t>(static_cast<int>(x) + 127) << 23);
+}
+// sigmoid(g) and 1 - sigmoid(g) = sigmoid(-g) of two values, each with its own
+// relative accuracy: with e = exp(-|g|) and r = 1 / (1 + e) they are r and e r, or
+// the other way round (the evaluation of sigmoid2, kept to both halves).
+__device__ __forceinline__ float2 sigmoid_both(float2 g, float2* rest) {
+  constexpr float kL2e = 1.4426950408889634f;
+  const float2 e = make_float2(ex2_approx(-fabsf(g.x) * kL2e), ex2_approx(-fabsf(g.y) * kL2e));
+  const float2 r = make_float2(__frcp_rn(1.0f + e.x), __frcp_rn(1.0f + e.y));
+  const float2 er = __fmul2_rn(e, r);
+  *rest = make_float2(g.x >= 0.0f ? er.x : r.x, g.y >= 0.0f ? er.y : r.y);
+  return make_float2(g.x >= 0.0f ? r.x : er.x, g.y >= 0.0f ? r.y : er.y);
+}
+
+// The largest |w| of the norm weights, by the 32 lanes of a warp.
+__device__ __forceinline__ float warp_absmax(const float* w, int lane) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(__ldg(w + lane + 32 * i)));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
+__device__ __forceinline__ void pdl_start() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// The raw row of x that a fragment's thread c covers: pairs 8 kk + 2 c + e and
+// dims 48 + 4 c .., 64 + 8 c .., 96 + 8 c ...
+struct RawRow {
+  float lo[6], hi[6], rest[20];
+};
+__device__ __forceinline__ void load_raw(RawRow& x, const uint16_t* row, int c, int P) {
+  if (row == nullptr) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) x.lo[i] = x.hi[i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 20; ++i) x.rest[i] = 0.f;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 6; ++i) {
+    const int j = 8 * (i >> 1) + 2 * c + (i & 1);
+    x.lo[i] = bf16_f32(__ldg(row + pair_lo(j, P)));
+    x.hi[i] = bf16_f32(__ldg(row + pair_hi(j, P)));
+  }
+  const uint2 r3 = __ldg(reinterpret_cast<const uint2*>(row + 48 + 4 * c));
+  const uint4 r4 = __ldg(reinterpret_cast<const uint4*>(row + 64 + 8 * c));
+  const uint4 r6 = __ldg(reinterpret_cast<const uint4*>(row + 96 + 8 * c));
+  const uint32_t w[10] = {r3.x, r3.y, r4.x, r4.y, r4.z, r4.w, r6.x, r6.y, r6.z, r6.w};
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+    x.rest[2 * i] = bf16_lo(w[i]);
+    x.rest[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+// Dim of rest[i] (thread c), and its weight.
+__device__ __forceinline__ int rest_dim(int i, int c) {
+  return i < 4 ? 48 + 4 * c + i : (i < 12 ? 64 + 8 * c + (i - 4) : 96 + 8 * c + (i - 12));
+}
+__device__ __forceinline__ float raw_rinv(const RawRow& x, float eps) {
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 6; ++i) s += x.lo[i] * x.lo[i] + x.hi[i] * x.hi[i];
+#pragma unroll
+  for (int i = 0; i < 20; ++i) s += x.rest[i] * x.rest[i];
+  s += __shfl_xor_sync(0xffffffffu, s, 1);
+  s += __shfl_xor_sync(0xffffffffu, s, 2);
+  return rsqrtf(s * (1.0f / kHeadDim) + eps);
+}
+
+
+// q' / cq of the two rows (r, r + 8) of a fragment, fp16 A operand in rope order;
+// `rot` is the rotation of row rr's pair i of this thread (pair 8 (i / 2) + 2 c +
+// (i & 1)), w the norm weights, icq = 1 / cq.
+template <typename Rot>
+__device__ __forceinline__ void q_fragment(uint32_t (&f)[8][4], const RawRow& x, int rr, float eps,
+                                           float icq, const float* w, int c, int P, Rot rot) {
+  const float rinv = raw_rinv(x, eps) * icq;
+#pragma unroll
+  for (int kk = 0; kk < 3; ++kk) {
+    float ul[2], uh[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int j = 8 * kk + 2 * c + e;
+      const float2 cs = rot(2 * kk + e);
+      const float u = x.lo[2 * kk + e] * rinv * __ldg(w + pair_lo(j, P));
+      const float v = x.hi[2 * kk + e] * rinv * __ldg(w + pair_hi(j, P));
+      ul[e] = u * cs.x - v * cs.y;
+      uh[e] = v * cs.x + u * cs.y;
+    }
+    f[kk][rr] = pack_f16x2(ul[0], ul[1]);
+    f[kk][2 + rr] = pack_f16x2(uh[0], uh[1]);
+  }
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+    const float2 ww = __ldg(reinterpret_cast<const float2*>(w + rest_dim(2 * i, c)));
+    f[3 + (i >> 1)][2 * (i & 1) + rr] =
+        pack_f16x2(x.rest[2 * i] * rinv * ww.x, x.rest[2 * i + 1] * rinv * ww.y);
+  }
 }
 
 }  // namespace snk
