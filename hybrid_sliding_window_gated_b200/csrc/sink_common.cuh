@@ -212,6 +212,13 @@ __device__ __forceinline__ void store_v_row(uint8_t* tile, int r, uint2 v, int l
 __device__ __forceinline__ float pow2i(float x) {
   return __uint_as_float(static_cast<uint32_t>(static_cast<int>(x) + 127) << 23);
 }
+// Exponent a of a V row: 0 where fp16 holds the row's entries as bf16 does.
+__device__ __forceinline__ float v_exp(float m) {
+  if (!(m > 0.0f) || (m >= 0.015625f && m < 32768.0f) || m == INFINITY) return 0.0f;
+  const int e = static_cast<int>((__float_as_uint(m) >> 23) & 255u) - 127;
+  return static_cast<float>(max(-100, min(100, -e)));
+}
+
 // sigmoid(g) and 1 - sigmoid(g) = sigmoid(-g) of two values, each with its own
 // relative accuracy: with e = exp(-|g|) and r = 1 / (1 + e) they are r and e r, or
 // the other way round (the evaluation of sigmoid2, kept to both halves).

@@ -72,7 +72,7 @@ inline int stage_size(int s8, int G) {
   return (n + 1023) & ~1023;
 }
 
-enum Site { kSiteFull = 0xD0, kSiteEmpty, kSiteForced };
+enum Site { kSiteFull = 0xD8, kSiteEmpty, kSiteForced };
 
 // Byte offset of 16-byte chunk c (0..15) of row s in a [half][row][64] tile with
 // 128-byte swizzle; `half` is the bytes of one half.

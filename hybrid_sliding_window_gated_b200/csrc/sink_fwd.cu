@@ -54,13 +54,6 @@ struct alignas(1024) FwdSmem {
 };
 static_assert(sizeof(FwdSmem) <= 115712, "two CTAs per SM");
 
-// Exponent a of a V row: 0 where fp16 holds the row's entries as bf16 does.
-__device__ __forceinline__ float v_exp(float m) {
-  if (!(m > 0.0f) || (m >= 0.015625f && m < 32768.0f) || m == INFINITY) return 0.0f;
-  const int e = static_cast<int>((__float_as_uint(m) >> 23) & 255u) - 127;
-  return static_cast<float>(max(-100, min(100, -e)));
-}
-
 template <int MH>
 __global__ void __launch_bounds__(kFwdThreads, 2) sink_fwd_kernel(const SinkFwdArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];

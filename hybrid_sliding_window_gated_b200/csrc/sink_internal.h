@@ -158,4 +158,11 @@ int launch_sink_bwd(const SinkBwdArgs& a, cudaStream_t stream);
 
 int launch_sink_fwd(const SinkFwdArgs& a, cudaStream_t stream);
 
+// Tensor maps of the tcgen05 forward: q, g, o in boxes of 64 tokens x 2 heads x 64
+// dims, k and v of 64 tokens x 64 dims, and of the first 16 tokens.
+struct SinkFwdMaps {
+  CUtensorMap q, k, v, g, o, ks, vs;
+};
+int launch_sink_fwd_tc(const SinkFwdMaps& m, const SinkFwdArgs& a, cudaStream_t stream);
+
 }  // namespace swa
