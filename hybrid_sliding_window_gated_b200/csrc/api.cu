@@ -748,7 +748,6 @@ int swa_sink_fwd(const swa_params_t* p, int32_t n_sink, const swa_bf16_t* q, con
   a.lse = lse;
   if ((rc = device_error_word(&a.err)) != SWA_OK) return rc;
   fill_inv_freq(p, a.inv_freq);
-  if (a.G % 2 != 0) return launch_sink_fwd(a, static_cast<cudaStream_t>(stream));
   SinkFwdMaps m;
   const uint64_t D = kHeadDim, T = p->T, B = p->B;
   const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
@@ -760,7 +759,7 @@ int swa_sink_fwd(const swa_params_t* p, int32_t n_sink, const swa_bf16_t* q, con
       (rc = encode_tmap_4d(&m.ks, k, D, p->Hkv, T, B, 64, 1, kMaxSink, 1, sw)) ||
       (rc = encode_tmap_4d(&m.vs, v, D, p->Hkv, T, B, 64, 1, kMaxSink, 1, sw)))
     return rc;
-  return launch_sink_fwd_tc(m, a, static_cast<cudaStream_t>(stream));
+  return launch_sink_fwd(m, a, static_cast<cudaStream_t>(stream));
 }
 
 size_t swa_sink_bwd_workspace_size(const swa_params_t* p, int32_t n_sink) {

@@ -613,9 +613,12 @@ __global__ void __launch_bounds__(kQThreads, 2) sink_bwd_q_kernel(const SinkBwdA
 
 // ------------------------------------------------------------ key-major block
 
+// P enters dV as 2^14 P: fp16 then keeps probabilities down to 2^-28 normal.
+constexpr float kPUp = 14.0f;
+
 // One block of 16 queries against a warp's 16 keys: P^T and dS^T, added into dv
 // and dk.  q' and dA rows of the block start at qt and dt, its row records at
-// `row`.  hide(key row, query column) masks, where `masked` says that any is.
+// `row`; am2 and fj carry 2^-kPUp, and dv 2^kPUp.  hide(key row, query column) masks, where `masked` says that any is.
 template <typename Hide, typename VFrag>
 __device__ __forceinline__ void key_block(float (&dk)[16][4], float (&dv)[16][4],
                                           const uint32_t (&kf)[8][4], VFrag vfrag, uint32_t qt,
@@ -654,7 +657,7 @@ __device__ __forceinline__ void key_block(float (&dk)[16][4], float (&dv)[16][4]
     for (int e = 0; e < 2; ++e) {
       const int col = 8 * n + 2 * c + e;
       const float4 x = row[col];  // lse log2(e), D 2^b, b
-      const float ei = ex2_approx(bm - x.z), Dn = x.y * am2;  // a whole exponent: exact
+      const float ei = ex2_approx(bm - x.z + kPUp), Dn = x.y * am2;  // a whole exponent: exact
 #pragma unroll
       for (int rr = 0; rr < 2; ++rr) {
         const int i = 2 * rr + e;
@@ -752,7 +755,8 @@ __global__ void __launch_bounds__(32 * kSWarps, 1) sink_bwd_sink_kernel(const Si
   float fj[2];
 #pragma unroll
   for (int rr = 0; rr < 2; ++rr)
-    fj[rr] = pow2i(fmaxf(fminf(am - a.va[chain * a.Tp + r + 8 * rr], 0.0f), -126.0f));
+    fj[rr] =
+        pow2i(fmaxf(fminf(am - a.va[chain * a.Tp + r + 8 * rr], 0.0f) - kPUp, -126.0f));
   float dk[16][4], dv[16][4];
 #pragma unroll
   for (int n = 0; n < 16; ++n) {
@@ -785,7 +789,7 @@ __global__ void __launch_bounds__(32 * kSWarps, 1) sink_bwd_sink_kernel(const Si
     __syncwarp();
     const int i0 = first + 16 * (u % per);
     key_block(dk, dv, kf, vfrag, smem_u32(sm.q[w][buf]), smem_u32(sm.d[w][buf]), sm.row[w][buf], sc,
-              bm, pow2i(am), fj, k_lane, t_lane, lane, true, [&](int key, int col) {
+              bm, pow2i(am) * pow2i(-kPUp), fj, k_lane, t_lane, lane, true, [&](int key, int col) {
                 return key >= a.n_sink || key > i0 + col - kWindow;
               });
     __syncwarp();
@@ -795,7 +799,7 @@ __global__ void __launch_bounds__(32 * kSWarps, 1) sink_bwd_sink_kernel(const Si
   // by the warps that wrote none, then by one of them
   float* part = reinterpret_cast<float*>(smem_raw);
   constexpr int kN = kMaxSink * kHeadDim;
-  const float fk = scale2(a.scale * cq, -(bm + am)), fv = scale2(1.0f, -bm);
+  const float fk = scale2(a.scale * cq, -(bm + am)), fv = scale2(1.0f, -bm - kPUp);
 #pragma unroll 1
   for (int half = kSWarps / 2; half >= 1; half >>= 1) {
     __syncthreads();
@@ -926,7 +930,8 @@ __global__ void __launch_bounds__(kKThreads, 2) sink_bwd_k_kernel(const SinkBwdA
   float fj[2];
 #pragma unroll
   for (int rr = 0; rr < 2; ++rr)
-    fj[rr] = pow2i(fmaxf(fminf(am - a.va[chain * a.Tp + j0 + r + 8 * rr], 0.0f), -126.0f));
+    fj[rr] =
+        pow2i(fmaxf(fminf(am - a.va[chain * a.Tp + j0 + r + 8 * rr], 0.0f) - kPUp, -126.0f));
   const uint32_t k_lane = (lane & 7) * kRowBytes + (lane >> 4) * 8 * kRowBytes +
                           ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
   const uint32_t t_lane = (lane & 7) * kRowBytes + ((lane >> 3) & 1) * 8 * kRowBytes +
@@ -941,7 +946,7 @@ __global__ void __launch_bounds__(kKThreads, 2) sink_bwd_k_kernel(const SinkBwdA
     for (; issued < min(total, kKStages); ++issued) issue(issued);
   const uint32_t va = smem_u32(sm.v) + 16 * w * kRowBytes + t_lane;
   auto vfrag = [&](int kk, uint32_t (&f)[4]) { ldsm_x4(va ^ (kk << 5), f); };
-  const float am2 = pow2i(am);
+  const float am2 = pow2i(am) * pow2i(-kPUp);
   float dk[16][4], dv[16][4];
 #pragma unroll
   for (int n = 0; n < 16; ++n) {
@@ -990,7 +995,7 @@ __global__ void __launch_bounds__(kKThreads, 2) sink_bwd_k_kernel(const SinkBwdA
   const int rows = min(16, a.T - j0);
   rope_fetch(sm.rope[w], a.k + raw, stride, rows, lane);
   // ---- true scale; the sinks' sums from the queries beyond the window
-  const float fk = scale2(a.scale * cq, -(bm + am)), fv = scale2(1.0f, -bm);
+  const float fk = scale2(a.scale * cq, -(bm + am)), fv = scale2(1.0f, -bm - kPUp);
   const bool add = a.n_sink > 0 && tile == 0 && w == 0;
   const float* sk = a.sink_sum + chain * 2 * kMaxSink * kHeadDim;
 #pragma unroll

@@ -212,8 +212,11 @@ __device__ __forceinline__ void store_v_row(uint8_t* tile, int r, uint2 v, int l
 __device__ __forceinline__ float pow2i(float x) {
   return __uint_as_float(static_cast<uint32_t>(static_cast<int>(x) + 127) << 23);
 }
-// Exponent a of a V row: 0 where fp16 holds the row's entries as bf16 does.
+// Exponent a of a V row: 0 where fp16 holds the row's entries as bf16 does, and
+// kZeroRow for a row of zeros, which no scale concerns.
+constexpr float kZeroRow = 127.0f;
 __device__ __forceinline__ float v_exp(float m) {
+  if (m == 0.0f) return kZeroRow;
   if (!(m > 0.0f) || (m >= 0.015625f && m < 32768.0f) || m == INFINITY) return 0.0f;
   const int e = static_cast<int>((__float_as_uint(m) >> 23) & 255u) - 127;
   return static_cast<float>(max(-100, min(100, -e)));
@@ -290,36 +293,6 @@ __device__ __forceinline__ float raw_rinv(const RawRow& x, float eps) {
   return rsqrtf(s * (1.0f / kHeadDim) + eps);
 }
 
-
-// q' / cq of the two rows (r, r + 8) of a fragment, fp16 A operand in rope order;
-// `rot` is the rotation of row rr's pair i of this thread (pair 8 (i / 2) + 2 c +
-// (i & 1)), w the norm weights, icq = 1 / cq.
-template <typename Rot>
-__device__ __forceinline__ void q_fragment(uint32_t (&f)[8][4], const RawRow& x, int rr, float eps,
-                                           float icq, const float* w, int c, int P, Rot rot) {
-  const float rinv = raw_rinv(x, eps) * icq;
-#pragma unroll
-  for (int kk = 0; kk < 3; ++kk) {
-    float ul[2], uh[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int j = 8 * kk + 2 * c + e;
-      const float2 cs = rot(2 * kk + e);
-      const float u = x.lo[2 * kk + e] * rinv * __ldg(w + pair_lo(j, P));
-      const float v = x.hi[2 * kk + e] * rinv * __ldg(w + pair_hi(j, P));
-      ul[e] = u * cs.x - v * cs.y;
-      uh[e] = v * cs.x + u * cs.y;
-    }
-    f[kk][rr] = pack_f16x2(ul[0], ul[1]);
-    f[kk][2 + rr] = pack_f16x2(uh[0], uh[1]);
-  }
-#pragma unroll
-  for (int i = 0; i < 10; ++i) {
-    const float2 ww = __ldg(reinterpret_cast<const float2*>(w + rest_dim(2 * i, c)));
-    f[3 + (i >> 1)][2 * (i & 1) + rr] =
-        pack_f16x2(x.rest[2 * i] * rinv * ww.x, x.rest[2 * i + 1] * rinv * ww.y);
-  }
-}
 
 }  // namespace snk
 }  // namespace swa

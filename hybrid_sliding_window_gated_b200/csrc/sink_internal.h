@@ -156,13 +156,11 @@ inline SinkBwdWs sink_bwd_ws(long long B, long long T, int Hq, int Hkv, int n_si
 
 int launch_sink_bwd(const SinkBwdArgs& a, cudaStream_t stream);
 
-int launch_sink_fwd(const SinkFwdArgs& a, cudaStream_t stream);
-
-// Tensor maps of the tcgen05 forward: q, g, o in boxes of 64 tokens x 2 heads x 64
+// Tensor maps of the forward: q, g, o in boxes of 64 tokens x 2 heads x 64
 // dims, k and v of 64 tokens x 64 dims, and of the first 16 tokens.
 struct SinkFwdMaps {
   CUtensorMap q, k, v, g, o, ks, vs;
 };
-int launch_sink_fwd_tc(const SinkFwdMaps& m, const SinkFwdArgs& a, cudaStream_t stream);
+int launch_sink_fwd(const SinkFwdMaps& m, const SinkFwdArgs& a, cudaStream_t stream);
 
 }  // namespace swa
