@@ -50,13 +50,14 @@
 namespace swa {
 namespace snk {
 
-constexpr float kNoScale = 100.0f;  // exponent of an all-zero row: takes part in no minimum
+constexpr float kNoScale = 126.0f;  // exponent of an all-zero row: takes part in no minimum
 
-// Exponent that brings m into [1, 2), within what two fp32 factors carry.
+// Exponent that brings m into [1, 2), or below 2^15 where that would take a factor
+// that is no normal fp32 number.
 __device__ __forceinline__ float scale_exp(float m) {
   if (!(m > 0.0f)) return kNoScale;
   const int e = static_cast<int>((__float_as_uint(m) >> 23) & 255u) - 127;
-  return static_cast<float>(max(-100, min(100, -e)));
+  return static_cast<float>(max(-113, min(126, -e)));
 }
 // v 2^x for whole x in [-252, 254], in two steps
 __device__ __forceinline__ float scale2(float v, float x) {

@@ -219,7 +219,7 @@ __device__ __forceinline__ float v_exp(float m) {
   if (m == 0.0f) return kZeroRow;
   if (!(m > 0.0f) || (m >= 0.015625f && m < 32768.0f) || m == INFINITY) return 0.0f;
   const int e = static_cast<int>((__float_as_uint(m) >> 23) & 255u) - 127;
-  return static_cast<float>(max(-100, min(100, -e)));
+  return static_cast<float>(max(-113, min(126, -e)));  // 2^-113: below 2^15 from any bf16
 }
 
 // sigmoid(g) and 1 - sigmoid(g) = sigmoid(-g) of two values, each with its own

@@ -809,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int s = 0; s < kSlots; ++s) scaled = scaled || (dist(s) >= 0 && sm.scaled[s] != 0);
       float am = 0.0f;
       if (scaled) {
-        am = 100.0f;
+        am = 126.0f;
         for (int s = 0; s < kSlots; ++s)
           if (dist(s) >= 0)
             am = fminf(am, fminf(sm.va[s * kTok + lane], sm.va[s * kTok + 32 + lane]));
@@ -902,7 +902,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!W(&sm.ofull[r], cnt & 1, kSiteOFull)) break;
       if (!W(&sm.gfull[qs], qph, kSiteGFull)) break;
       tc_fence_after();
-      const float il = 1.0f / l * pow2i(-am);
+      // V of all keys below 2^-64: the result's factor in two steps, both normal
+      const float split = am > 64.0f ? 64.0f : 0.0f;
+      const float il = 1.0f / l * pow2i(split - am);
 #pragma unroll 1
       for (int ch = 0; ch < kHeadDim / 32; ++ch) {
         uint32_t ov[32];
@@ -938,10 +940,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (p == 0.0f || key0 + e >= a.T) continue;
                 const uint16_t* vrow =
                     a.v + ((static_cast<long long>(c.b) * a.T + key0 + e) * a.Hkv + c.kvh) * kHeadDim;
+                float f = 1.0f;
                 if (scaled) {  // P carries 2^-a of its key (the ring's record may have moved on)
                   uint32_t m = 0;
                   for (int i = 0; i < kHeadDim; ++i) m = max(m, vrow[i] & 0x7fffu);
-                  p *= pow2i(v_exp(__uint_as_float(min(m, 0x7f80u) << 16)));
+                  f = pow2i(v_exp(__uint_as_float(min(m, 0x7f80u) << 16)));
                 }
                 const uint4* vr4 = reinterpret_cast<const uint4*>(vrow + 32 * ch);
 #pragma unroll
@@ -950,8 +953,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const uint32_t ww[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
                   for (int q = 0; q < 4; ++q) {
-                    o[8 * y + 2 * q] = fmaf(p, bf16_lo(ww[q]), o[8 * y + 2 * q]);
-                    o[8 * y + 2 * q + 1] = fmaf(p, bf16_hi(ww[q]), o[8 * y + 2 * q + 1]);
+                    o[8 * y + 2 * q] = fmaf(p, f * bf16_lo(ww[q]), o[8 * y + 2 * q]);
+                    o[8 * y + 2 * q + 1] = fmaf(p, f * bf16_hi(ww[q]), o[8 * y + 2 * q + 1]);
                   }
                 }
               }
@@ -960,6 +963,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(o[i]);
           }
+        }
+        if (split != 0.0f) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            ov[i] = __float_as_uint(__uint_as_float(ov[i]) * pow2i(-split));
         }
         if (ch + 1 == kHeadDim / 32) {
           tc_fence_before();
