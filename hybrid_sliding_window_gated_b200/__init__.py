@@ -116,7 +116,12 @@ def _ptr(t):
 
 
 def _stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if not torch.cuda.is_initialized():
+        torch.cuda.init()
+    # the pointer alone: a torch.cuda.Stream object around it costs 3 us
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _check(rc, where):
@@ -130,6 +135,15 @@ def _need(where, device, **tensors):
     must be a contiguous CUDA tensor on `device` with the dtype and at least
     that many elements; the kernels take its pointer and the sizes in the
     parameter block, so anything else would be misread or overrun."""
+    index = device.index
+    for t, dtype, n in tensors.values():  # one pass; a call in order ends here
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
+            break
+        if n > 0 and not (t.is_cuda and t.get_device() == index and t.is_contiguous()
+                          and t.numel() >= n):
+            break
+    else:
+        return
     for name, (t, dtype, n) in tensors.items():
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{where}: {name} must be a torch.Tensor")
