@@ -40,16 +40,20 @@ constexpr int kQStride = 68;             // words per packed q' row
 constexpr int kOStride = 136;            // floats per partial-O row
 
 struct Group {
-  uint32_t qa[2 * kDecMaxGroup][kQStride];  // q' as bf16 pairs: heads, then their remainders
   float scratch[4][kHeadDim];
   float mw[4][kDecMaxGroup], lw[4][kDecMaxGroup];
 };
 struct Control {
   Group grp[kGroups];
-  uint64_t full[kMaxStages], empty[kMaxStages], never;
+  // rows: q, the new k and v, rotation, position; full: rings, sinks, g
+  uint64_t rows[kMaxStages], full[kMaxStages], empty[kMaxStages], never;
   int abort;
 };
 static_assert(4 * kDecMaxGroup * kOStride * 4 <= 2 * kHalf, "partial O does not fit the K ring");
+
+// Behind Control, for each group: q' as bf16 pairs, [2 G][kQStride] words (the heads,
+// then their remainders).
+__host__ __device__ inline int qa_bytes(int G) { return 2 * G * kQStride * 4; }
 
 // A stage: K ring, V ring (two 64-dim halves each), K and V sinks (two halves
 // of s8 rows each), q and g rows, the new k and v, the rotation, the position.
@@ -72,7 +76,7 @@ inline int stage_size(int s8, int G) {
   return (n + 1023) & ~1023;
 }
 
-enum Site { kSiteFull = 0xD8, kSiteEmpty, kSiteForced };
+enum Site { kSiteFull = 0xD8, kSiteEmpty, kSiteForced, kSiteRows };
 
 // Byte offset of 16-byte chunk c (0..15) of row s in a [half][row][64] tile with
 // 128-byte swizzle; `half` is the bytes of one half.
@@ -109,14 +113,19 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   lo = pack_bf16x2(x - bf16_lo(hi), y - bf16_hi(hi));
 }
 
-__device__ __forceinline__ void process_unit(const Stage& st, Group& gp, const SinkDecArgs& a,
-                                             int n, int kvh, int gi, int lw, int lane) {
+// One unit by one group.  q' and the new k' depend on the rows alone, which land
+// first: they are worked out while the rings are still on their way.  False where a
+// wait ran out.
+__device__ __forceinline__ bool process_unit(const Stage& st, Group& gp, uint32_t* qa,
+                                             const SinkDecArgs& a, int n, int kvh, int gi, int lw,
+                                             int lane,
+                                             uint64_t* rows, uint64_t* full, uint32_t phase,
+                                             volatile int* abort) {
   const int bar_id = 1 + gi;
+  if (!group_and(mbar_wait(rows, phase, abort, a.err, kSiteRows), bar_id)) return false;
   const long long p = *st.pos();
-  if (p < 0) {  // the same value for the whole group
-    if (lw == 0 && lane == 0) atomicCAS(a.err, 0, kDevErrBadPosition);
-    return;
-  }
+  const bool bad = p < 0;  // the same value for the whole group
+  if (bad && lw == 0 && lane == 0) atomicCAS(a.err, 0, kDevErrBadPosition);
   const int s0 = static_cast<int>(p & (kWindow - 1));
   const int owner = s0 >> 5;
   const bool sink_warp = a.n_sink > 0 && lw == ((owner + 2) & 3) && p >= kWindow;
@@ -134,19 +143,26 @@ __device__ __forceinline__ void process_unit(const Stage& st, Group& gp, const S
     norm_rope_row(x, a.wq, a.eps, gp.scratch[lw], lane, a.half_rot, cs, sn);
     uint32_t hi, lo;
     split2(x[0], x[1], hi, lo);
-    gp.qa[h][2 * lane] = hi;
-    gp.qa[kDecMaxGroup + h][2 * lane] = lo;
+    qa[h * kQStride + 2 * lane] = hi;
+    qa[(a.G + h) * kQStride + 2 * lane] = lo;
     split2(x[2], x[3], hi, lo);
-    gp.qa[h][2 * lane + 1] = hi;
-    gp.qa[kDecMaxGroup + h][2 * lane + 1] = lo;
+    qa[h * kQStride + 2 * lane + 1] = hi;
+    qa[(a.G + h) * kQStride + 2 * lane + 1] = lo;
   }
-  // The new token's row into slot s0, in shared memory and in the caches.
+  uint2 kp = make_uint2(0u, 0u), vp = kp;
   if (lw == owner) {
     float x[4];
     load4(st.kn() + 4 * lane, x);
     norm_rope_row(x, a.wk, a.eps, gp.scratch[lw], lane, a.half_rot, cs, sn);
-    const uint2 kp = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-    const uint2 vp = *reinterpret_cast<const uint2*>(st.vn() + 4 * lane);
+    kp = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+    vp = *reinterpret_cast<const uint2*>(st.vn() + 4 * lane);
+  }
+  // the rings have landed, and q' is visible to the group
+  if (!group_and(mbar_wait(full, phase, abort, a.err, kSiteFull), bar_id)) return false;
+  if (bad) return true;
+  // The new token's row into slot s0, in shared memory and in the caches.  Each warp
+  // reads its own 32 slots only, so what it changes there needs no group barrier.
+  if (lw == owner) {
     const uint32_t off = tile_off(s0, lane >> 1, kHalf) + (lane & 1) * 8;
     *reinterpret_cast<uint2*>(st.k() + off) = kp;
     *reinterpret_cast<uint2*>(st.v() + off) = vp;
@@ -159,32 +175,28 @@ __device__ __forceinline__ void process_unit(const Stage& st, Group& gp, const S
       *reinterpret_cast<uint2*>(a.k_sink + srow) = kp;
       *reinterpret_cast<uint2*>(a.v_sink + srow) = vp;
     }
-    __syncwarp();
   }
   // Slots that hold no token of the sequence may hold anything: their V rows
   // become zeros, since P = 0 does not hide an infinity or a NaN.
   {
     const int s = 32 * lw + lane;
     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-    bool wrote = false;
     if (p - ((p - s) & (kWindow - 1)) < 0) {
 #pragma unroll
       for (int c = 0; c < 16; ++c) *reinterpret_cast<uint4*>(st.v() + tile_off(s, c, kHalf)) = z;
-      wrote = true;
     }
     if (sink_warp && lane >= seen && lane < a.s8) {
 #pragma unroll
       for (int c = 0; c < 16; ++c)
         *reinterpret_cast<uint4*>(st.vs() + tile_off(lane, c, a.s8 * 128)) = z;
-      wrote = true;
     }
-    if (wrote) fence_proxy_async_smem();  // before a later copy into this stage
   }
-  group_and(true, bar_id);  // q', the new row and the zeros are visible to the group
+  __syncwarp();
 
   // ---- S = q' K^T: 4 n-tiles of the ring, 2 of the sinks on one warp
   const int grp = lane >> 2, tig = lane & 3;
   const bool row_ok = grp < a.G;
+  const uint32_t *qh = qa + grp * kQStride + tig, *ql = qh + a.G * kQStride;
   float acc[6][4];
 #pragma unroll
   for (int j = 0; j < 6; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
@@ -195,10 +207,10 @@ __device__ __forceinline__ void process_unit(const Stage& st, Group& gp, const S
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int kk = 2 * kp2 + e;
-      q0[e] = row_ok ? gp.qa[grp][8 * kk + tig] : 0u;
-      q1[e] = row_ok ? gp.qa[kDecMaxGroup + grp][8 * kk + tig] : 0u;
-      q2[e] = row_ok ? gp.qa[grp][8 * kk + 4 + tig] : 0u;
-      q3[e] = row_ok ? gp.qa[kDecMaxGroup + grp][8 * kk + 4 + tig] : 0u;
+      q0[e] = row_ok ? qh[8 * kk] : 0u;
+      q1[e] = row_ok ? ql[8 * kk] : 0u;
+      q2[e] = row_ok ? qh[8 * kk + 4] : 0u;
+      q3[e] = row_ok ? ql[8 * kk + 4] : 0u;
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -207,12 +219,27 @@ __device__ __forceinline__ void process_unit(const Stage& st, Group& gp, const S
       mma_16816(acc[j], q0[0], q1[0], q2[0], q3[0], b[0], b[1]);
       mma_16816(acc[j], q0[1], q1[1], q2[1], q3[1], b[2], b[3]);
     }
-    if (sink_warp) {
+  }
+  // The sinks in loops of their own: a branch inside the ring's would keep its loads
+  // and products from overlapping (28 -> 39 us at 256 sequences).
+  if (sink_warp) {
+#pragma unroll
+    for (int kp2 = 0; kp2 < 4; ++kp2) {
+      uint32_t q0[2], q1[2], q2[2], q3[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int kk = 2 * kp2 + e;
+        q0[e] = row_ok ? qh[8 * kk] : 0u;
+        q1[e] = row_ok ? ql[8 * kk] : 0u;
+        q2[e] = row_ok ? qh[8 * kk + 4] : 0u;
+        q3[e] = row_ok ? ql[8 * kk + 4] : 0u;
+      }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        if (8 * j >= a.s8) break;
+        // keys 8 .. 15 of an 8-row cache are masked and read rows 0 .. 7 again
+        const int r = (8 * j < a.s8 ? 8 * j : 0) + (lane & 7);
         uint32_t b[4];
-        ldsm_x4(ksbase + tile_off(8 * j + (lane & 7), 4 * kp2 + (lane >> 3), a.s8 * 128), b);
+        ldsm_x4(ksbase + tile_off(r, 4 * kp2 + (lane >> 3), a.s8 * 128), b);
         mma_16816(acc[4 + j], q0[0], q1[0], q2[0], q3[0], b[0], b[1]);
         mma_16816(acc[4 + j], q0[1], q1[1], q2[1], q3[1], b[2], b[3]);
       }
@@ -261,9 +288,14 @@ __device__ __forceinline__ void process_unit(const Stage& st, Group& gp, const S
     ldsm_x4_trans(vbase + tile_off(32 * lw + lane, nd, kHalf), b);
     mma_16816(oacc[nd], ph[0], pl[0], ph[1], pl[1], b[0], b[1]);
     mma_16816(oacc[nd], ph[2], pl[2], ph[3], pl[3], b[2], b[3]);
-    if (sink_warp) {
-      ldsm_x4_trans(vsbase + tile_off(srow, nd, a.s8 * 128), b);
+  }
+  if (sink_warp) {
+#pragma unroll
+    for (int nd = 0; nd < 16; nd += 2) {  // matrices 2, 3: the next eight dims
+      uint32_t b[4];
+      ldsm_x4_trans(vsbase + tile_off(srow, nd + (lane >> 4), a.s8 * 128), b);
       mma_16816(oacc[nd], ph[4], pl[4], ph[5], pl[5], b[0], b[1]);
+      mma_16816(oacc[nd + 1], ph[4], pl[4], ph[5], pl[5], b[2], b[3]);
     }
   }
   group_and(true, bar_id);  // every warp is done with the K ring: reuse it
@@ -279,7 +311,7 @@ __device__ __forceinline__ void process_unit(const Stage& st, Group& gp, const S
       gp.lw[lw][grp] = l;
     }
   }
-  fence_proxy_async_smem();  // these writes before a later copy into the stage
+  fence_proxy_async_smem();  // this thread's writes before a later copy into the stage
   group_and(true, bar_id);
 
   // ---- o = (sum_w O_w 2^(m_w - m)) / (sum_w l_w 2^(m_w - m)) * sigmoid(g)
@@ -313,6 +345,7 @@ __device__ __forceinline__ void process_unit(const Stage& st, Group& gp, const S
                               4 * lane) =
         make_uint2(pack_bf16x2(ov[0], ov[1]), pack_bf16x2(ov[2], ov[3]));
   }
+  return true;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -331,7 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(&sm.full[s], 2);  // the copies' expect_tx arrive + the position
+      mbar_init(&sm.rows[s], 2);  // the copies' expect_tx arrive + the position
+      mbar_init(&sm.full[s], 1);
       mbar_init(&sm.empty[s], 1);
     }
     mbar_init(&sm.never, 1);
@@ -350,9 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       prefetch_tensormap(&tm_v);
     }
     const uint32_t row_bytes = kHeadDim * 2;
-    const uint32_t bytes = 4 * kHalf + a.s8 * 512 + 2 * a.G * row_bytes + 2 * row_bytes;
-    int issued[kMaxStages] = {0};
-    bool ok = true;
+    const uint32_t bytes = 4 * kHalf + a.s8 * 512 + a.G * row_bytes;
+    int issued = 0;
     long long seq = -1, p = 0;
     float2 rot = make_float2(1.0f, 0.0f);
     int s = 0, round = 0;
@@ -360,15 +393,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool w = true;
       if (lane == 0 && round > 0)
         w = mbar_wait(&sm.empty[s], (round - 1) & 1, abort, a.err, kSiteEmpty);
-      if (!__shfl_sync(0xffffffffu, w ? 1 : 0, 0)) {
-        ok = false;
-        break;
-      }
+      if (!__shfl_sync(0xffffffffu, w ? 1 : 0, 0)) break;
       const long long u = u0 + i;
       const int n = static_cast<int>(u / a.Hkv), kvh = static_cast<int>(u - u / a.Hkv * a.Hkv);
       const Stage st{base + s * a.stage_bytes, a.s8, a.G};
       if (lane == 0) {
-        uint64_t* full = &sm.full[s];
+        uint64_t *rows = &sm.rows[s], *full = &sm.full[s];
+        const long long qrow = (static_cast<long long>(n) * a.Hq + kvh * a.G) * kHeadDim;
+        const long long kvrow = (static_cast<long long>(n) * a.Hkv + kvh) * kHeadDim;
+        mbar_arrive_expect_tx(rows, (a.G + 2) * row_bytes);
+        bulk_load(st.q(), a.q + qrow, a.G * row_bytes, rows);
+        bulk_load(st.kn(), a.k_new + kvrow, row_bytes, rows);
+        bulk_load(st.vn(), a.v_new + kvrow, row_bytes, rows);
         mbar_arrive_expect_tx(full, bytes);
         tma_load_4d(st.k(), &tm_k, full, 0, 0, kvh, n);
         tma_load_4d(st.k() + kHalf, &tm_k, full, 64, 0, kvh, n);
@@ -380,13 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_4d(st.vs(), &tm_vs, full, 0, 0, kvh, n);
           tma_load_4d(st.vs() + a.s8 * 128, &tm_vs, full, 64, 0, kvh, n);
         }
-        const long long qrow = (static_cast<long long>(n) * a.Hq + kvh * a.G) * kHeadDim;
-        const long long kvrow = (static_cast<long long>(n) * a.Hkv + kvh) * kHeadDim;
-        bulk_load(st.q(), a.q + qrow, a.G * row_bytes, full);
         bulk_load(st.g(), a.g + qrow, a.G * row_bytes, full);
-        bulk_load(st.kn(), a.k_new + kvrow, row_bytes, full);
-        bulk_load(st.vn(), a.v_new + kvrow, row_bytes, full);
-        ++issued[s];
+        issued = i + 1;
       }
       if (n != seq) {
         seq = n;
@@ -397,30 +428,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) *st.pos() = p;
       if (lane < a.half_rot) st.rot()[lane] = rot;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.full[s]);
+      if (lane == 0) mbar_arrive(&sm.rows[s]);
       if (++s == a.stages) {
         s = 0;
         ++round;
       }
     }
-    if (!ok && lane == 0) {
-      for (int i = 0; i < a.stages; ++i)
-        if (issued[i] > 0) mbar_wait_drain(&sm.full[i], (issued[i] - 1) & 1);
+    // no copy is in flight when the CTA ends, whatever the consumers did
+    if (lane == 0) {
+      for (int i = max(0, issued - a.stages); i < issued; ++i) {
+        mbar_wait_drain(&sm.rows[i % a.stages], (i / a.stages) & 1);
+        mbar_wait_drain(&sm.full[i % a.stages], (i / a.stages) & 1);
+      }
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------- consumer group
     const int gi = (warp - 1) >> 2, lw = (warp - 1) & 3;
+    uint32_t* qa = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(&sm + 1) +
+                                               gi * qa_bytes(a.G));
     bool live = true;
     if (a.flags & SWA_FLAG_FORCE_TIMEOUT)
       live = group_and(mbar_wait(&sm.never, 0, abort, a.err, kSiteForced), 1 + gi);
     for (int i = gi; live && i < n_units; i += kGroups) {
       const int s = i % a.stages;
-      const bool got = mbar_wait(&sm.full[s], (i / a.stages) & 1, abort, a.err, kSiteFull);
-      if (!group_and(got, 1 + gi)) break;
       const long long u = u0 + i;
       const int n = static_cast<int>(u / a.Hkv), kvh = static_cast<int>(u - u / a.Hkv * a.Hkv);
-      process_unit(Stage{base + s * a.stage_bytes, a.s8, a.G}, sm.grp[gi], a, n, kvh, gi, lw, lane);
+      if (!process_unit(Stage{base + s * a.stage_bytes, a.s8, a.G}, sm.grp[gi], qa, a, n, kvh, gi, lw,
+                        lane, &sm.rows[s], &sm.full[s], (i / a.stages) & 1, abort))
+        break;
       group_and(true, 1 + gi);
       if (lw == 0 && lane == 0) mbar_arrive(&sm.empty[s]);
     }
@@ -474,10 +510,10 @@ int launch_sink_decode(const CUtensorMap& tk, const CUtensorMap& tv, const CUten
   int rc = current_device_info(&di);
   if (rc != SWA_OK) return rc;
   constexpr int kLimit = 232448;
-  constexpr int kFixed = static_cast<int>(sizeof(snd::Control)) + 1024;
+  const int fixed = static_cast<int>(sizeof(snd::Control)) + snd::kGroups * snd::qa_bytes(a.G) + 1024;
   a.stage_bytes = snd::stage_size(a.s8, a.G);
   // Three units in flight where they fit (up to 8 sinks, or 16 with few heads), else two.
-  a.stages = 3 * a.stage_bytes + kFixed <= kLimit ? 3 : 2;
+  a.stages = 3 * a.stage_bytes + fixed <= kLimit ? 3 : 2;
   static std::atomic<int> configured[64];
   if (!configured[di.device].load(std::memory_order_acquire)) {
     cudaError_t e = cudaFuncSetAttribute(snd::sink_decode_kernel,
@@ -488,7 +524,7 @@ int launch_sink_decode(const CUtensorMap& tk, const CUtensorMap& tv, const CUten
   const long long units = static_cast<long long>(a.N) * a.Hkv;
   const long long grid = units < di.num_sms ? units : di.num_sms;
   return launch_dependent(snd::sink_decode_kernel, static_cast<unsigned>(grid), snd::kThreads,
-                          static_cast<size_t>(a.stages) * a.stage_bytes + kFixed, stream, tk, tv,
+                          static_cast<size_t>(a.stages) * a.stage_bytes + fixed, stream, tk, tv,
                           tks, tvs, a);
 }
 
