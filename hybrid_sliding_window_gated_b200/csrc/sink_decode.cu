@@ -10,10 +10,17 @@
 // What bounds it: memory.  A unit is one (sequence, KV head): 64 KiB of ring,
 // 512 bytes per sink and 2.5 KiB of new rows.  As in the plain decode step a
 // persistent CTA streams its units: a producer warp keeps the next ones in
-// flight by TMA (128-byte swizzle) and two groups of four warps take alternate
-// units, warp w of a group slots 32 w .. 32 w + 31; one of the warps also takes
-// the sinks, as one more 8- or 16-key block of its own softmax, so they cost no
-// further merge.
+// flight by TMA (128-byte swizzle) and two groups take alternate units.  A group is
+// five warps: warp w < 4 attends over slots 32 w .. 32 w + 31, the fifth over the
+// sinks, and the five partial results are joined by their maxima and sums.  A unit's
+// rows (q, the new k and v, position) land on a barrier of their own, so q' and k'
+// are worked out while its rings are still on their way.
+//
+// Measured, 256 sequences x 32 / 8 heads, 4 sinks, 146 MB a step (20 steps over four
+// caches in a graph): 27.7 us, 5.3 TB/s.  Sinks on one of the four ring warps, in
+// loops behind the ring's: 31.4 us; inside the ring's loops, where the branch keeps
+// loads and products from overlapping, and with two units in flight: 39.5 us.  With
+// 16 sinks two units fit: 33.8 us.
 //
 // Two bf16 terms at no cost.  The tensor core's A operand has 16 rows and a
 // group at most eight heads, so rows 0-7 carry the bf16 of q' and rows 8-15
@@ -33,15 +40,17 @@ namespace swa {
 namespace snd {
 
 constexpr int kGroups = 2;
-constexpr int kThreads = 32 * (1 + 4 * kGroups);
+constexpr int kGroupWarps = 5;           // four for the ring, one for the sinks
+constexpr int kThreads = 32 * (1 + kGroupWarps * kGroups);
 constexpr int kMaxStages = 3;
 constexpr int kHalf = kWindow * 64 * 2;  // 128 slots x 64 dims (one TMA box)
 constexpr int kQStride = 68;             // words per packed q' row
 constexpr int kOStride = 136;            // floats per partial-O row
 
 struct Group {
-  float scratch[4][kHeadDim];
-  float mw[4][kDecMaxGroup], lw[4][kDecMaxGroup];
+  float scratch[kGroupWarps][kHeadDim];
+  float mw[kGroupWarps][kDecMaxGroup], lw[kGroupWarps][kDecMaxGroup];
+  uint2 k_row[32], v_row[32];  // the new token's k' and v, four dims each
 };
 struct Control {
   Group grp[kGroups];
@@ -49,7 +58,7 @@ struct Control {
   uint64_t rows[kMaxStages], full[kMaxStages], empty[kMaxStages], never;
   int abort;
 };
-static_assert(4 * kDecMaxGroup * kOStride * 4 <= 2 * kHalf, "partial O does not fit the K ring");
+static_assert(kGroupWarps * kDecMaxGroup * kOStride * 4 <= 2 * kHalf, "partial O does not fit the K ring");
 
 // Behind Control, for each group: q' as bf16 pairs, [2 G][kQStride] words (the heads,
 // then their remainders).
@@ -93,13 +102,13 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-// Barrier over a group's 128 threads that also ANDs v across them.
+// Barrier over a group's 160 threads that also ANDs v across them.
 __device__ __forceinline__ bool group_and(bool v, int id) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, %2, 128, p;\n\t"
+      "bar.red.and.pred q, %2, 160, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
       : "r"(static_cast<uint32_t>(v)), "r"(id)
@@ -113,94 +122,19 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   lo = pack_bf16x2(x - bf16_lo(hi), y - bf16_hi(hi));
 }
 
-// One unit by one group.  q' and the new k' depend on the rows alone, which land
-// first: they are worked out while the rings are still on their way.  False where a
-// wait ran out.
-__device__ __forceinline__ bool process_unit(const Stage& st, Group& gp, uint32_t* qa,
-                                             const SinkDecArgs& a, int n, int kvh, int gi, int lw,
-                                             int lane,
-                                             uint64_t* rows, uint64_t* full, uint32_t phase,
-                                             volatile int* abort) {
-  const int bar_id = 1 + gi;
-  if (!group_and(mbar_wait(rows, phase, abort, a.err, kSiteRows), bar_id)) return false;
-  const long long p = *st.pos();
-  const bool bad = p < 0;  // the same value for the whole group
-  if (bad && lw == 0 && lane == 0) atomicCAS(a.err, 0, kDevErrBadPosition);
-  const int s0 = static_cast<int>(p & (kWindow - 1));
-  const int owner = s0 >> 5;
-  const bool sink_warp = a.n_sink > 0 && lw == ((owner + 2) & 3) && p >= kWindow;
-  const int seen = p - kWindow >= a.n_sink ? a.n_sink : static_cast<int>(p - kWindow) + 1;
-
-  float cs = 1.0f, sn = 0.0f;
-  if (lane < a.half_rot) {
-    const float2 r = st.rot()[lane];
-    cs = r.x;
-    sn = r.y;
-  }
-  for (int h = lw; h < a.G; h += 4) {
-    float x[4];
-    load4(st.q() + h * kHeadDim + 4 * lane, x);
-    norm_rope_row(x, a.wq, a.eps, gp.scratch[lw], lane, a.half_rot, cs, sn);
-    uint32_t hi, lo;
-    split2(x[0], x[1], hi, lo);
-    qa[h * kQStride + 2 * lane] = hi;
-    qa[(a.G + h) * kQStride + 2 * lane] = lo;
-    split2(x[2], x[3], hi, lo);
-    qa[h * kQStride + 2 * lane + 1] = hi;
-    qa[(a.G + h) * kQStride + 2 * lane + 1] = lo;
-  }
-  uint2 kp = make_uint2(0u, 0u), vp = kp;
-  if (lw == owner) {
-    float x[4];
-    load4(st.kn() + 4 * lane, x);
-    norm_rope_row(x, a.wk, a.eps, gp.scratch[lw], lane, a.half_rot, cs, sn);
-    kp = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-    vp = *reinterpret_cast<const uint2*>(st.vn() + 4 * lane);
-  }
-  // the rings have landed, and q' is visible to the group
-  if (!group_and(mbar_wait(full, phase, abort, a.err, kSiteFull), bar_id)) return false;
-  if (bad) return true;
-  // The new token's row into slot s0, in shared memory and in the caches.  Each warp
-  // reads its own 32 slots only, so what it changes there needs no group barrier.
-  if (lw == owner) {
-    const uint32_t off = tile_off(s0, lane >> 1, kHalf) + (lane & 1) * 8;
-    *reinterpret_cast<uint2*>(st.k() + off) = kp;
-    *reinterpret_cast<uint2*>(st.v() + off) = vp;
-    const long long unit = static_cast<long long>(n) * a.Hkv + kvh;
-    const long long row = (unit * kWindow + s0) * kHeadDim + 4 * lane;
-    *reinterpret_cast<uint2*>(a.k_cache + row) = kp;
-    *reinterpret_cast<uint2*>(a.v_cache + row) = vp;
-    if (p < a.n_sink) {
-      const long long srow = (unit * a.n_sink + p) * kHeadDim + 4 * lane;
-      *reinterpret_cast<uint2*>(a.k_sink + srow) = kp;
-      *reinterpret_cast<uint2*>(a.v_sink + srow) = vp;
-    }
-  }
-  // Slots that hold no token of the sequence may hold anything: their V rows
-  // become zeros, since P = 0 does not hide an infinity or a NaN.
-  {
-    const int s = 32 * lw + lane;
-    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-    if (p - ((p - s) & (kWindow - 1)) < 0) {
+// One warp's share of a unit: S = q' K^T over NT n-tiles of 8 keys, the softmax of its
+// own keys in log2 units (maximum m, sum l of head row grp), and the partial O = P V.
+// krow + kstep j is the K row of n-tile j that this lane fetches, vrow its V row.  Keys
+// that valid(key) refuses are masked; their V rows are finite.
+template <int NT, typename Valid>
+__device__ __forceinline__ void attend(uint32_t kbase, uint32_t vbase, int half, int krow, int kstep,
+                                       int vrow, const uint32_t* qh, const uint32_t* ql,
+                                       bool row_ok, float scale_log2, int lane, Valid&& valid,
+                                       float& m, float& l, float (&oacc)[16][4]) {
+  const int tig = lane & 3;
+  float acc[NT][4];
 #pragma unroll
-      for (int c = 0; c < 16; ++c) *reinterpret_cast<uint4*>(st.v() + tile_off(s, c, kHalf)) = z;
-    }
-    if (sink_warp && lane >= seen && lane < a.s8) {
-#pragma unroll
-      for (int c = 0; c < 16; ++c)
-        *reinterpret_cast<uint4*>(st.vs() + tile_off(lane, c, a.s8 * 128)) = z;
-    }
-  }
-  __syncwarp();
-
-  // ---- S = q' K^T: 4 n-tiles of the ring, 2 of the sinks on one warp
-  const int grp = lane >> 2, tig = lane & 3;
-  const bool row_ok = grp < a.G;
-  const uint32_t *qh = qa + grp * kQStride + tig, *ql = qh + a.G * kQStride;
-  float acc[6][4];
-#pragma unroll
-  for (int j = 0; j < 6; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
-  const uint32_t kbase = smem_u32(st.k()), ksbase = smem_u32(st.ks());
+  for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
 #pragma unroll
   for (int kp2 = 0; kp2 < 4; ++kp2) {
     uint32_t q0[2], q1[2], q2[2], q3[2];
@@ -213,61 +147,29 @@ __device__ __forceinline__ bool process_unit(const Stage& st, Group& gp, uint32_
       q3[e] = row_ok ? ql[8 * kk + 4] : 0u;
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < NT; ++j) {
       uint32_t b[4];
-      ldsm_x4(kbase + tile_off(32 * lw + 8 * j + (lane & 7), 4 * kp2 + (lane >> 3), kHalf), b);
+      ldsm_x4(kbase + tile_off(krow + kstep * j, 4 * kp2 + (lane >> 3), half), b);
       mma_16816(acc[j], q0[0], q1[0], q2[0], q3[0], b[0], b[1]);
       mma_16816(acc[j], q0[1], q1[1], q2[1], q3[1], b[2], b[3]);
     }
   }
-  // The sinks in loops of their own: a branch inside the ring's would keep its loads
-  // and products from overlapping (28 -> 39 us at 256 sequences).
-  if (sink_warp) {
+  m = -INFINITY;
 #pragma unroll
-    for (int kp2 = 0; kp2 < 4; ++kp2) {
-      uint32_t q0[2], q1[2], q2[2], q3[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int kk = 2 * kp2 + e;
-        q0[e] = row_ok ? qh[8 * kk] : 0u;
-        q1[e] = row_ok ? ql[8 * kk] : 0u;
-        q2[e] = row_ok ? qh[8 * kk + 4] : 0u;
-        q3[e] = row_ok ? ql[8 * kk + 4] : 0u;
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        // keys 8 .. 15 of an 8-row cache are masked and read rows 0 .. 7 again
-        const int r = (8 * j < a.s8 ? 8 * j : 0) + (lane & 7);
-        uint32_t b[4];
-        ldsm_x4(ksbase + tile_off(r, 4 * kp2 + (lane >> 3), a.s8 * 128), b);
-        mma_16816(acc[4 + j], q0[0], q1[0], q2[0], q3[0], b[0], b[1]);
-        mma_16816(acc[4 + j], q0[1], q1[1], q2[1], q3[1], b[2], b[3]);
-      }
-    }
-  }
-  // ---- softmax of this warp's keys, in log2 units
-  float m = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < 6; ++j)
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      bool valid;
-      if (j < 4) {
-        const int s = 32 * lw + 8 * j + 2 * tig + e;
-        valid = p - ((p - s) & (kWindow - 1)) >= 0;
-      } else {
-        valid = sink_warp && 8 * (j - 4) + 2 * tig + e < seen;
-      }
-      acc[j][e] = valid ? (acc[j][e] + acc[j][e + 2]) * a.scale_log2 : -INFINITY;
+      acc[j][e] =
+          valid(8 * j + 2 * tig + e) ? (acc[j][e] + acc[j][e + 2]) * scale_log2 : -INFINITY;
       m = fmaxf(m, acc[j][e]);
     }
   m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
   const float mu = m == -INFINITY ? 0.0f : m;
-  float l = 0.0f;
-  uint32_t ph[6], pl[6];
+  l = 0.0f;
+  uint32_t ph[NT], pl[NT];
 #pragma unroll
-  for (int j = 0; j < 6; ++j) {
+  for (int j = 0; j < NT; ++j) {
     const float p0 = ex2_approx(acc[j][0] - mu), p1 = ex2_approx(acc[j][1] - mu);
     l += p0 + p1;
     split2(p0, p1, ph[j], pl[j]);
@@ -275,32 +177,127 @@ __device__ __forceinline__ bool process_unit(const Stage& st, Group& gp, uint32_
   }
   l += __shfl_xor_sync(0xffffffffu, l, 1);
   l += __shfl_xor_sync(0xffffffffu, l, 2);
-
-  // ---- partial O = P V
-  float oacc[16][4];
-  const uint32_t vbase = smem_u32(st.v()), vsbase = smem_u32(st.vs());
-  // sink keys 8 .. 15 of an 8-row cache have P = 0 and read rows 0 .. 7 again
-  const int srow = a.s8 == 16 ? (lane & 15) : (lane & 7);
 #pragma unroll
-  for (int nd = 0; nd < 16; ++nd) {
+  for (int nd = 0; nd < 16; ++nd)
     oacc[nd][0] = oacc[nd][1] = oacc[nd][2] = oacc[nd][3] = 0.0f;
-    uint32_t b[4];
-    ldsm_x4_trans(vbase + tile_off(32 * lw + lane, nd, kHalf), b);
-    mma_16816(oacc[nd], ph[0], pl[0], ph[1], pl[1], b[0], b[1]);
-    mma_16816(oacc[nd], ph[2], pl[2], ph[3], pl[3], b[2], b[3]);
-  }
-  if (sink_warp) {
+  if constexpr (NT == 4) {  // lane: V row of keys 0 .. 31, one n-tile of dims at a time
 #pragma unroll
-    for (int nd = 0; nd < 16; nd += 2) {  // matrices 2, 3: the next eight dims
+    for (int nd = 0; nd < 16; ++nd) {
       uint32_t b[4];
-      ldsm_x4_trans(vsbase + tile_off(srow, nd + (lane >> 4), a.s8 * 128), b);
-      mma_16816(oacc[nd], ph[4], pl[4], ph[5], pl[5], b[0], b[1]);
-      mma_16816(oacc[nd + 1], ph[4], pl[4], ph[5], pl[5], b[2], b[3]);
+      ldsm_x4_trans(vbase + tile_off(vrow, nd, half), b);
+      mma_16816(oacc[nd], ph[0], pl[0], ph[1], pl[1], b[0], b[1]);
+      mma_16816(oacc[nd], ph[2], pl[2], ph[3], pl[3], b[2], b[3]);
+    }
+  } else {  // lane: V row of keys 0 .. 15, two n-tiles of dims at a time
+#pragma unroll
+    for (int nd = 0; nd < 16; nd += 2) {
+      uint32_t b[4];
+      ldsm_x4_trans(vbase + tile_off(vrow, nd + (lane >> 4), half), b);
+      mma_16816(oacc[nd], ph[0], pl[0], ph[1], pl[1], b[0], b[1]);
+      mma_16816(oacc[nd + 1], ph[0], pl[0], ph[1], pl[1], b[2], b[3]);
     }
   }
+}
+
+// One unit by one group of five warps.  q' (warps 0-3) and the new k' (warp 4) depend
+// on the rows alone, which land first: they are worked out while the rings are still
+// on their way.  Then warps 0-3 take 32 ring slots each and warp 4 the sinks.  False
+// where a wait ran out.
+__device__ __forceinline__ bool process_unit(const Stage& st, Group& gp, uint32_t* qa,
+                                             const SinkDecArgs& a, int n, int kvh, int gi, int lw,
+                                             int lane, uint64_t* rows, uint64_t* full,
+                                             uint32_t phase, volatile int* abort) {
+  const int bar_id = 1 + gi;
+  if (!group_and(mbar_wait(rows, phase, abort, a.err, kSiteRows), bar_id)) return false;
+  const long long p = *st.pos();
+  const bool bad = p < 0;  // the same value for the whole group
+  if (bad && lw == 0 && lane == 0) atomicCAS(a.err, 0, kDevErrBadPosition);
+  const int s0 = static_cast<int>(p & (kWindow - 1));
+  // sinks outside the window (0: none, and warp 4 has no part)
+  const int seen =
+      p - kWindow >= a.n_sink ? a.n_sink : max(0, static_cast<int>(p - kWindow) + 1);
+  const int parts = seen > 0 ? 5 : 4;
+
+  float cs = 1.0f, sn = 0.0f;
+  if (lane < a.half_rot) {
+    const float2 r = st.rot()[lane];
+    cs = r.x;
+    sn = r.y;
+  }
+  if (lw < 4) {
+    for (int h = lw; h < a.G; h += 4) {
+      float x[4];
+      load4(st.q() + h * kHeadDim + 4 * lane, x);
+      norm_rope_row(x, a.wq, a.eps, gp.scratch[lw], lane, a.half_rot, cs, sn);
+      uint32_t hi, lo;
+      split2(x[0], x[1], hi, lo);
+      qa[h * kQStride + 2 * lane] = hi;
+      qa[(a.G + h) * kQStride + 2 * lane] = lo;
+      split2(x[2], x[3], hi, lo);
+      qa[h * kQStride + 2 * lane + 1] = hi;
+      qa[(a.G + h) * kQStride + 2 * lane + 1] = lo;
+    }
+  } else {
+    float x[4];
+    load4(st.kn() + 4 * lane, x);
+    norm_rope_row(x, a.wk, a.eps, gp.scratch[lw], lane, a.half_rot, cs, sn);
+    gp.k_row[lane] = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+    gp.v_row[lane] = *reinterpret_cast<const uint2*>(st.vn() + 4 * lane);
+  }
+  // the rings have landed, and q' and the new row are visible to the group
+  if (!group_and(mbar_wait(full, phase, abort, a.err, kSiteFull), bar_id)) return false;
+  if (bad) return true;
+  // Each warp reads its own slots only, so what it changes there needs no barrier.
+  // Slots that hold no token of the sequence may hold anything: their V rows become
+  // zeros, since P = 0 does not hide an infinity or a NaN.
+  const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+  if (lw < 4) {
+    const int s = 32 * lw + lane;
+    if (p - ((p - s) & (kWindow - 1)) < 0) {
+#pragma unroll
+      for (int c = 0; c < 16; ++c) *reinterpret_cast<uint4*>(st.v() + tile_off(s, c, kHalf)) = z;
+    }
+    if (lw == s0 >> 5) {  // the new token's row, into its slot and the caches
+      const uint2 kp = gp.k_row[lane], vp = gp.v_row[lane];
+      const uint32_t off = tile_off(s0, lane >> 1, kHalf) + (lane & 1) * 8;
+      *reinterpret_cast<uint2*>(st.k() + off) = kp;
+      *reinterpret_cast<uint2*>(st.v() + off) = vp;
+      const long long unit = static_cast<long long>(n) * a.Hkv + kvh;
+      const long long row = (unit * kWindow + s0) * kHeadDim + 4 * lane;
+      *reinterpret_cast<uint2*>(a.k_cache + row) = kp;
+      *reinterpret_cast<uint2*>(a.v_cache + row) = vp;
+      if (p < a.n_sink) {
+        const long long srow = (unit * a.n_sink + p) * kHeadDim + 4 * lane;
+        *reinterpret_cast<uint2*>(a.k_sink + srow) = kp;
+        *reinterpret_cast<uint2*>(a.v_sink + srow) = vp;
+      }
+    }
+  } else if (lane >= seen && lane < a.s8) {
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+      *reinterpret_cast<uint4*>(st.vs() + tile_off(lane, c, a.s8 * 128)) = z;
+  }
+  __syncwarp();
+
+  const int grp = lane >> 2, tig = lane & 3;
+  const bool row_ok = grp < a.G;
+  const uint32_t *qh = qa + grp * kQStride + tig, *ql = qh + a.G * kQStride;
+  float m = -INFINITY, l = 0.0f, oacc[16][4];
+  if (lw < 4) {
+    attend<4>(smem_u32(st.k()), smem_u32(st.v()), kHalf, 32 * lw + (lane & 7), 8, 32 * lw + lane,
+              qh, ql, row_ok, a.scale_log2, lane,
+              [&](int key) { return p - ((p - (32 * lw + key)) & (kWindow - 1)) >= 0; }, m, l,
+              oacc);
+  } else if (seen > 0) {
+    // an 8-row cache has no keys 8 .. 15: rows 0 .. 7 again, masked
+    const bool wide = a.s8 == 16;
+    attend<2>(smem_u32(st.ks()), smem_u32(st.vs()), a.s8 * 128, lane & 7, wide ? 8 : 0,
+              lane & (wide ? 15 : 7), qh, ql, row_ok, a.scale_log2, lane,
+              [&](int key) { return key < seen; }, m, l, oacc);
+  }
   group_and(true, bar_id);  // every warp is done with the K ring: reuse it
-  float* part = reinterpret_cast<float*>(st.k());  // [4][kDecMaxGroup][kOStride]
-  if (row_ok) {
+  float* part = reinterpret_cast<float*>(st.k());  // [parts][kDecMaxGroup][kOStride]
+  if (row_ok && lw < parts) {
     float* dst = part + (lw * kDecMaxGroup + grp) * kOStride + 2 * tig;
 #pragma unroll
     for (int nd = 0; nd < 16; ++nd)
@@ -315,25 +312,23 @@ __device__ __forceinline__ bool process_unit(const Stage& st, Group& gp, uint32_
   group_and(true, bar_id);
 
   // ---- o = (sum_w O_w 2^(m_w - m)) / (sum_w l_w 2^(m_w - m)) * sigmoid(g)
-  for (int h = lw; h < a.G; h += 4) {
+  for (int h = lw; h < a.G; h += kGroupWarps) {
     float mx = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) mx = fmaxf(mx, gp.mw[w][h]);
-    float f[4], lsum = 0.0f;
+    for (int w = 0; w < kGroupWarps; ++w)
+      if (w < parts) mx = fmaxf(mx, gp.mw[w][h]);
+    float lsum = 0.0f, y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      f[w] = gp.mw[w][h] == -INFINITY ? 0.0f : ex2_approx(gp.mw[w][h] - mx);
-      lsum += f[w] * gp.lw[w][h];
-    }
-    float y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < kGroupWarps; ++w) {
+      if (w >= parts) continue;
+      const float f = gp.mw[w][h] == -INFINITY ? 0.0f : ex2_approx(gp.mw[w][h] - mx);
+      lsum += f * gp.lw[w][h];
       const float4 v4 =
           *reinterpret_cast<const float4*>(part + (w * kDecMaxGroup + h) * kOStride + 4 * lane);
-      y[0] += f[w] * v4.x;
-      y[1] += f[w] * v4.y;
-      y[2] += f[w] * v4.z;
-      y[3] += f[w] * v4.w;
+      y[0] += f * v4.x;
+      y[1] += f * v4.y;
+      y[2] += f * v4.z;
+      y[3] += f * v4.w;
     }
     const float inv_l = 1.0f / lsum;
     float gx[4];
@@ -444,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------- consumer group
-    const int gi = (warp - 1) >> 2, lw = (warp - 1) & 3;
+    const int gi = (warp - 1) / kGroupWarps, lw = (warp - 1) % kGroupWarps;
     uint32_t* qa = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(&sm + 1) +
                                                gi * qa_bytes(a.G));
     bool live = true;
