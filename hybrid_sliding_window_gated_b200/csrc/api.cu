@@ -797,7 +797,9 @@ int swa_sink_bwd(const swa_params_t* p, int32_t n_sink, const swa_bf16_t* q, con
   a.G = p->Hq / p->Hkv;
   a.n_sink = n_sink;
   a.half_rot = p->rot_dim / 2;
-  a.chunks = n_sink > 0 ? (a.Tp + kSinkChunk - 1) / kSinkChunk : 0;
+  a.chunk = sink_chunk(p->T);
+  a.chunks = n_sink > 0 ? (a.Tp + a.chunk - 1) / a.chunk : 0;
+  a.head_parts = sink_head_parts(static_cast<long long>(p->B) * p->Hkv * a.tiles, a.G);
   a.scale = score_scale(p);
   a.scale_log2 = a.scale * 1.4426950408889634f;
   a.eps = p->eps;

@@ -139,13 +139,16 @@ __global__ void __launch_bounds__(256) sink_bwd_kv_kernel(const SinkBwdArgs a) {
   }
 }
 
-// One warp per 16 tokens of a query head, two rows at a time and four dims per
-// lane (64 registers, so 32 warps per SM: 241 us for 16,384 tokens of 32 heads, against
-// 266 with four rows and 16 warps): q' and dA as operand rows, dg, and the rows' lse and exponent b.  Bound by
-// memory: 1 KiB read and 768 bytes written per row.
+// One warp per 16 tokens of a query head, two rows at a time and four dims per lane:
+// q' and dA as operand rows, dg, and the rows' lse and exponent b.  Bound by memory:
+// 1 KiB read and 768 bytes written per row.  The next two rows are on their way to
+// shared memory while a pair is worked on (190 us for 16,384 tokens of 32 heads,
+// 241 with plain loads and as many warps).
 __global__ void __launch_bounds__(256, 4) sink_bwd_rows_kernel(const SinkBwdArgs a) {
+  constexpr int kN = 2;
+  __shared__ __align__(16) uint8_t in[8][2][4][kN * kRowBytes];  // q, g, dO, o as they are
   // operand rows are put together here and leave in 16-byte pieces
-  __shared__ __align__(16) uint8_t stage[8][2][8 * kRowBytes];
+  __shared__ __align__(16) uint8_t stage[8][2][kN * kRowBytes];
   pdl_start();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, P = a.half_rot;
   const long long gw = static_cast<long long>(blockIdx.x) * 8 + warp;
@@ -155,6 +158,30 @@ __global__ void __launch_bounds__(256, 4) sink_bwd_rows_kernel(const SinkBwdArgs
   const int per = a.Tp >> 4, b = static_cast<int>(grp / per);
   if (b >= a.B) return;
   const int t0 = static_cast<int>(grp - static_cast<long long>(b) * per) * 16;
+  const uint16_t* src[4] = {a.q, a.g, a.dO, a.o};
+  const auto fetch = [&](int i, int buf) {
+    const int t = t0 + i + (lane >> 4);
+    const long long at = ((static_cast<long long>(b) * a.T + min(t, a.T - 1)) * a.Hq + hq) *
+                             kHeadDim + 8 * (lane & 15);
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      cp_async16(smem_u32(in[warp][buf][x]) + 16 * lane, src[x] + at, t < a.T);
+    cp_async_commit();
+  };
+  const float* lse = a.lse + (static_cast<long long>(b) * a.Hq + hq) * a.T;
+  float2 rot[kN];
+  float l2[kN];
+  const auto fetch_row = [&](int i) {  // rotations and lse, held in registers
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+      const int t = t0 + i + e;
+      rot[e] = lane < kMaxPairs ? __ldg(a.rot + static_cast<long long>(t) * kMaxPairs + lane)
+                                : make_float2(1.f, 0.f);
+      l2[e] = t < a.T ? __ldg(lse + t) * 1.4426950408889634f : 0.f;
+    }
+  };
+  fetch(0, 0);
+  fetch_row(0);
   const float icq = 1.0f / pow2_ceil(warp_absmax(a.wq, lane));
   const int dlo = lane < kMaxPairs ? pair_lo(lane, P) : 0;
   const int dhi = lane < kMaxPairs ? pair_hi(lane, P) : 0;
@@ -166,42 +193,41 @@ __global__ void __launch_bounds__(256, 4) sink_bwd_rows_kernel(const SinkBwdArgs
   }
   const long long out = (static_cast<long long>(b) * a.Hq + hq) * a.Tp + t0;
   float bm = kNoScale;
-  constexpr int kN = 2;
 #pragma unroll 1
   for (int i = 0; i < 16; i += kN) {
-    KRow x[kN];
-    uint2 g2[kN], d2[kN], o2[kN];
-    float2 rot[kN];
-    float l2[kN];
-#pragma unroll
-    for (int e = 0; e < kN; ++e) {
-      const int t = t0 + i + e;
-      const bool real = t < a.T;
-      const long long at = ((static_cast<long long>(b) * a.T + t) * a.Hq + hq) * kHeadDim;
-      x[e] = load_k_row(real ? a.q + at : nullptr, lane, dlo, dhi);
-      g2[e] = d2[e] = o2[e] = make_uint2(0u, 0u);
-      l2[e] = 0.f;
-      if (real) {
-        g2[e] = __ldg(reinterpret_cast<const uint2*>(a.g + at + 4 * lane));
-        d2[e] = __ldg(reinterpret_cast<const uint2*>(a.dO + at + 4 * lane));
-        o2[e] = __ldg(reinterpret_cast<const uint2*>(a.o + at + 4 * lane));
-        l2[e] = __ldg(a.lse + (static_cast<long long>(b) * a.Hq + hq) * a.T + t) *
-                1.4426950408889634f;
-      }
-      rot[e] = lane < kMaxPairs ? __ldg(a.rot + static_cast<long long>(t) * kMaxPairs + lane)
-                                : make_float2(1.f, 0.f);
+    const int buf = (i / kN) & 1;
+    if (i + kN < 16) {
+      fetch(i + kN, buf ^ 1);
+      cp_async_wait<1>();
+    } else {
+      cp_async_wait<0>();
     }
+    __syncwarp();  // the rows have landed, and the stage has been read out
     float2 u0[kN], u1[kN];
     float m[kN];
+    KRow x[kN];
 #pragma unroll
     for (int e = 0; e < kN; ++e) {
+      const uint8_t* row = &in[warp][buf][0][0] + e * kRowBytes;
+      constexpr int kTensor = kN * kRowBytes;
+      const uint16_t* qrow = reinterpret_cast<const uint16_t*>(row);
+      x[e].lo = x[e].hi = 0;
+      x[e].rest = make_uint2(0u, 0u);
+      if (lane < kMaxPairs) {
+        x[e].lo = qrow[dlo];
+        x[e].hi = qrow[dhi];
+      }
+      if (lane < 20) x[e].rest = *reinterpret_cast<const uint2*>(qrow + kRopeDims + 4 * lane);
+      const uint2 g2 = *reinterpret_cast<const uint2*>(row + kTensor + 8 * lane);
+      const uint2 d2 = *reinterpret_cast<const uint2*>(row + 2 * kTensor + 8 * lane);
+      const uint2 o2 = *reinterpret_cast<const uint2*>(row + 3 * kTensor + 8 * lane);
       float2 n0, n1;
-      const float2 s0 = sigmoid_both(make_float2(bf16_lo(g2[e].x), bf16_hi(g2[e].x)), &n0);
-      const float2 s1 = sigmoid_both(make_float2(bf16_lo(g2[e].y), bf16_hi(g2[e].y)), &n1);
-      const float2 d0 = make_float2(bf16_lo(d2[e].x), bf16_hi(d2[e].x));
-      const float2 d1 = make_float2(bf16_lo(d2[e].y), bf16_hi(d2[e].y));
-      const float2 q0 = make_float2(bf16_lo(o2[e].x), bf16_hi(o2[e].x));
-      const float2 q1 = make_float2(bf16_lo(o2[e].y), bf16_hi(o2[e].y));
+      const float2 s0 = sigmoid_both(make_float2(bf16_lo(g2.x), bf16_hi(g2.x)), &n0);
+      const float2 s1 = sigmoid_both(make_float2(bf16_lo(g2.y), bf16_hi(g2.y)), &n1);
+      const float2 d0 = make_float2(bf16_lo(d2.x), bf16_hi(d2.x));
+      const float2 d1 = make_float2(bf16_lo(d2.y), bf16_hi(d2.y));
+      const float2 q0 = make_float2(bf16_lo(o2.x), bf16_hi(o2.x));
+      const float2 q1 = make_float2(bf16_lo(o2.y), bf16_hi(o2.y));
       u0[e] = __fmul2_rn(d0, s0);
       u1[e] = __fmul2_rn(d1, s1);
       const float2 y0 = __fmul2_rn(__fmul2_rn(d0, q0), n0), y1 = __fmul2_rn(__fmul2_rn(d1, q1), n1);
@@ -215,29 +241,29 @@ __global__ void __launch_bounds__(256, 4) sink_bwd_rows_kernel(const SinkBwdArgs
       // magnitudes order as their bits do
       m[e] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
     }
-    store_k_rows<kN>(stage[warp][0], i & 7, x, lane, w_lo, w_hi, w_rest, rot, a.eps);
+    // the stage holds rows i & 7 .. of an eight-row tile
+    uint8_t* qt = stage[warp][0] - (i & 7) * kRowBytes;
+    uint8_t* dt = stage[warp][1] - (i & 7) * kRowBytes;
+    store_k_rows<kN>(qt, i & 7, x, lane, w_lo, w_hi, w_rest, rot, a.eps);
     const int md = lane >> 3, c = (lane & 7) >> 1, q = 2 * (lane & 1);
 #pragma unroll
     for (int e = 0; e < kN; ++e) {
       const float be = scale_exp(m[e]), f = pow2i(be);
       bm = fminf(bm, be);
       const int r = (i & 7) + e;
-      *reinterpret_cast<uint32_t*>(stage[warp][1] + row_off(r, 4 * md + q) + 4 * c) =
+      *reinterpret_cast<uint32_t*>(dt + row_off(r, 4 * md + q) + 4 * c) =
           pack_f16x2(u0[e].x * f, u0[e].y * f);
-      *reinterpret_cast<uint32_t*>(stage[warp][1] + row_off(r, 4 * md + q + 1) + 4 * c) =
+      *reinterpret_cast<uint32_t*>(dt + row_off(r, 4 * md + q + 1) + 4 * c) =
           pack_f16x2(u1[e].x * f, u1[e].y * f);
       if (lane == 0) a.row[out + i + e] = make_float4(l2[e], 0.f, be, 0.f);
     }
+    if (i + kN < 16) fetch_row(i + kN);
     __syncwarp();
-    const int at = (i & 7) * kRowBytes + 16 * lane;
-#pragma unroll
-    for (int y = 0; y < kN * kRowBytes / 512; ++y) {
-      *reinterpret_cast<uint4*>(a.qr + (out + i - (i & 7)) * kRowBytes + at + 512 * y) =
-          *reinterpret_cast<const uint4*>(stage[warp][0] + at + 512 * y);
-      *reinterpret_cast<uint4*>(a.dr + (out + i - (i & 7)) * kRowBytes + at + 512 * y) =
-          *reinterpret_cast<const uint4*>(stage[warp][1] + at + 512 * y);
-    }
-    // the next rows use another part of the stage
+    const long long at = (out + i) * kRowBytes + 16 * lane;
+    *reinterpret_cast<uint4*>(a.qr + at) =
+        *reinterpret_cast<const uint4*>(stage[warp][0] + 16 * lane);
+    *reinterpret_cast<uint4*>(a.dr + at) =
+        *reinterpret_cast<const uint4*>(stage[warp][1] + 16 * lane);
   }
   if (lane == 0) a.bmin[out >> 4] = bm;
 }
@@ -418,14 +444,19 @@ static_assert(sizeof(QSmem) <= 115712, "two CTAs per SM");
 
 enum BwdSite { kSiteBQ = 0xF0, kSiteBFull, kSiteBEmpty, kSiteBTile };
 
+// One CTA per (batch row, KV head, 64 queries), or per part of the head's query heads
+// where those are too few for the SMs (sink_head_parts).
 __global__ void __launch_bounds__(kQThreads, 2) sink_bwd_q_kernel(const SinkBwdArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   QSmem& sm = *reinterpret_cast<QSmem*>(smem_raw);
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int r = lane >> 2, c = lane & 3, P = a.half_rot;
-  const int tile = static_cast<int>(blockIdx.x % a.tiles);
-  const long long chain = blockIdx.x / a.tiles;
+  const int part = static_cast<int>(blockIdx.x % a.head_parts);
+  const long long unit = blockIdx.x / a.head_parts;
+  const int tile = static_cast<int>(unit % a.tiles);
+  const long long chain = unit / a.tiles;
   const int b = static_cast<int>(chain / a.Hkv), kvh = static_cast<int>(chain % a.Hkv);
+  const int h0 = a.G * part / a.head_parts, h1 = a.G * (part + 1) / a.head_parts;
   const int t0 = tile * kSinkTile;
   const int s0 = max(0, t0 - kWindow);      // first key row in shared memory
   const int shift = s0 - (t0 - kWindow);    // rows of the band before the sequence
@@ -462,7 +493,7 @@ __global__ void __launch_bounds__(kQThreads, 2) sink_bwd_q_kernel(const SinkBwdA
     if (i >= kBand && sinks) e = a.va[chain * a.Tp + i - kBand];
     sm.vf[i] = pow2i(fmaxf(fminf(am - e, 0.0f), -126.0f));
   }
-  if (tid == 0) a.amin[chain * a.tiles + tile] = am;
+  if (tid == 0 && part == 0) a.amin[chain * a.tiles + tile] = am;
   const float cq = pow2_ceil(warp_absmax(a.wq, lane)), ck = pow2_ceil(warp_absmax(a.wk, lane));
   const float sc = a.scale_log2 * cq * ck;
   volatile int* abort = &sm.abort;
@@ -480,7 +511,7 @@ __global__ void __launch_bounds__(kQThreads, 2) sink_bwd_q_kernel(const SinkBwdA
   const long long stride = static_cast<long long>(a.Hq) * kHeadDim;
   const int rows = min(16, a.T - i0);  // none or fewer past the sequence's end
 #pragma unroll 1
-  for (int h = 0; h < a.G; ++h) {
+  for (int h = h0; h < h1; ++h) {
     const int hq = kvh * a.G + h;
     const long long hrow = (static_cast<long long>(b) * a.Hq + hq) * a.Tp + i0;
     // ---- q' and dA as A fragments: words c of the rows' chunks
@@ -508,7 +539,7 @@ __global__ void __launch_bounds__(kQThreads, 2) sink_bwd_q_kernel(const SinkBwdA
     }
     // the next head's rows, and this one's raw q for the end, towards L2
     {
-      const long long nx = hrow * kRowBytes + (h + 1 < a.G ? static_cast<long long>(a.Tp) * kRowBytes : 0);
+      const long long nx = hrow * kRowBytes + (h + 1 < h1 ? static_cast<long long>(a.Tp) * kRowBytes : 0);
       asm volatile("prefetch.global.L2 [%0];" ::"l"(a.qr + nx + 128 * lane));
       asm volatile("prefetch.global.L2 [%0];" ::"l"(a.dr + nx + 128 * lane));
       const int t = min(i0 + (lane >> 1), a.T - 1);
@@ -722,7 +753,7 @@ struct alignas(1024) SSmem {
 };
 static_assert(sizeof(SSmem) >= kSWarps / 2 * kMaxSink * kHeadDim * 2 * 4, "partial sums");
 
-// One CTA per (batch row, KV head, chunk of kSinkChunk tokens); its warps take the
+// One CTA per (batch row, KV head, chunk of a.chunk tokens); its warps take the
 // 16-query blocks of all heads in turn and are added up at the end.
 __global__ void __launch_bounds__(32 * kSWarps, 1) sink_bwd_sink_kernel(const SinkBwdArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -732,7 +763,7 @@ __global__ void __launch_bounds__(32 * kSWarps, 1) sink_bwd_sink_kernel(const Si
   const int chunk = static_cast<int>(blockIdx.x % a.chunks);
   const long long chain = blockIdx.x / a.chunks;
   const int b = static_cast<int>(chain / a.Hkv), kvh = static_cast<int>(chain % a.Hkv);
-  const int ta = chunk * kSinkChunk, tb = min(a.Tp, ta + kSinkChunk);
+  const int ta = chunk * a.chunk, tb = min(a.Tp, ta + a.chunk);
   for (int i = tid; i < 2 * kSinkBytes / 16; i += 32 * kSWarps) {
     const int at = i & (kSinkBytes / 16 - 1);
     const uint8_t* src = (i < kSinkBytes / 16 ? a.kr : a.vr) + chain * a.Tp * kRowBytes;
@@ -1044,7 +1075,8 @@ __global__ void __launch_bounds__(1024) sink_bwd_w_kernel(const SinkBwdArgs a) {
   pdl_start();
   const int d = threadIdx.x & 15, s = threadIdx.x >> 4, dim = 16 * blockIdx.x + d;
   const float* src = blockIdx.y == 0 ? a.dwq_part : a.dwk_part;
-  const long long n = static_cast<long long>(a.B) * a.Hkv * a.tiles;
+  const long long n = static_cast<long long>(a.B) * a.Hkv * a.tiles *
+                      (blockIdx.y == 0 ? a.head_parts : 1);
   float x = 0.f;
 #pragma unroll 8
   for (long long i = s; i < n; i += 64) x += src[i * kHeadDim + dim];
@@ -1083,14 +1115,14 @@ int launch_sink_bwd(const SinkBwdArgs& a, cudaStream_t stream) {
   const long long tiles = static_cast<long long>(a.B) * a.Hkv * a.tiles;
   const long long chains = static_cast<long long>(a.B) * a.Hkv;
   const long long row_warps = tokens / 16 * a.Hq;
-  if (row_warps / 8 > 0x7fffffffLL || tokens / 8 > 0x7fffffffLL || tiles > 0x7fffffffLL || chains * 16 > 0x7fffffffLL)
+  if (row_warps / 8 > 0x7fffffffLL || tokens / 8 > 0x7fffffffLL || tiles * a.head_parts > 0x7fffffffLL || chains * 16 > 0x7fffffffLL)
     return SWA_ERR_UNSUPPORTED;
   const auto grid = [](long long n) { return static_cast<unsigned>(n); };
   rc = launch_dependent(snk::sink_bwd_kv_kernel, grid((tokens + 7) / 8), 256, 0, stream, a);
   if (rc == SWA_OK)
     rc = launch_dependent(snk::sink_bwd_rows_kernel, grid((row_warps + 7) / 8), 256, 0, stream, a);
   if (rc == SWA_OK)
-    rc = launch_dependent(snk::sink_bwd_q_kernel, grid(tiles), snk::kQThreads, sizeof(snk::QSmem),
+    rc = launch_dependent(snk::sink_bwd_q_kernel, grid(tiles * a.head_parts), snk::kQThreads, sizeof(snk::QSmem),
                           stream, a);
   if (rc == SWA_OK && a.n_sink > 0) {
     rc = launch_dependent(snk::sink_bwd_sink_kernel, grid(chains * a.chunks), 32 * snk::kSWarps,

@@ -84,7 +84,8 @@ struct SinkBwdArgs {
   int n_sink;
   int half_rot;
   int tiles;              // kSinkTile-token tiles per sequence
-  int chunks;             // token chunks of the sinks' pass per (batch row, KV head)
+  int chunk, chunks;      // the sinks' pass: tokens per CTA, CTAs per (batch row, KV head)
+  int head_parts;         // CTAs of the query-major pass per (KV head, tile)
   float scale, scale_log2, eps;
   const uint16_t* q;
   const uint16_t* k;
@@ -111,16 +112,26 @@ struct SinkBwdArgs {
   float4* row;            // [B, Hq, Tp]: lse log2(e), D 2^b, b
   float* bmin;            // [B, Hq, Tp / 16]: least b of 16 rows
   float* amin;            // [B, Hkv, tiles]: least a of the keys the tile's queries may see
-  float* dwq_part;        // [B Hkv tiles, D]
-  float* dwk_part;
+  float* dwq_part;        // [B Hkv tiles head_parts, D]
+  float* dwk_part;        // [B Hkv tiles, D]
   float* sink_part;       // [B, Hkv, chunks, 2, kMaxSink, D]: dk' (rope order), dv (split order)
   float* sink_sum;        // [B, Hkv, 2, kMaxSink, D]
   int* err;
   double inv_freq[kMaxPairs];
 };
 
-// Tokens per CTA of the sinks' pass.
-constexpr int kSinkChunk = 512;
+// Tokens per CTA of the sinks' pass: fewer where a sequence is short, since a CTA
+// takes about 4 us + 3 us per 64 tokens of 4 heads.  The length alone decides, so a
+// sequence's gradients are the same bits in every batch.  2 x 1001 tokens of 8 / 2
+// heads: 28 us with 512 tokens per CTA, 16 us with 128; 16,384 tokens of 32 / 8: 62 us.
+inline int sink_chunk(long long T) { return T <= 4096 ? 128 : 512; }
+// Parts of a KV head's G query heads in the query-major pass: as many as keep its CTAs
+// to two per SM of 148 (each reads the tile's keys again).  2 x 1001 tokens of 8 / 2
+// heads, 64 tiles: 39 us in one part, 19 us in four.
+inline int sink_head_parts(long long units, int G) {
+  const long long n = 296 / units;
+  return static_cast<int>(n < 1 ? 1 : (n > G ? G : n));
+}
 
 struct SinkBwdWs {
   size_t rot, kr, vr, va, qr, dr, row, bmin, amin, dwq, dwk, part, sum, total;
@@ -129,7 +140,8 @@ inline SinkBwdWs sink_bwd_ws(long long B, long long T, int Hq, int Hkv, int n_si
   const size_t Tp = static_cast<size_t>((T + kSinkTile - 1) / kSinkTile) * kSinkTile;
   const size_t tiles = Tp / kSinkTile, hk = static_cast<size_t>(B) * Hkv;
   const size_t hq = static_cast<size_t>(B) * Hq;
-  const size_t chunks = n_sink > 0 ? (Tp + kSinkChunk - 1) / kSinkChunk : 0;
+  const size_t chunks = n_sink > 0 ? (Tp + sink_chunk(T) - 1) / sink_chunk(T) : 0;
+  const size_t parts = hk == 0 || tiles == 0 ? 1 : sink_head_parts(hk * tiles, Hq / Hkv);
   SinkBwdWs w{};
   size_t at = 0;
   const auto take = [&at](size_t n) {
@@ -146,7 +158,7 @@ inline SinkBwdWs sink_bwd_ws(long long B, long long T, int Hq, int Hkv, int n_si
   w.row = take(hq * Tp * 16);
   w.bmin = take(hq * Tp / 16 * 4);
   w.amin = take(hk * tiles * 4);
-  w.dwq = take(hk * tiles * kHeadDim * 4);
+  w.dwq = take(hk * tiles * parts * kHeadDim * 4);
   w.dwk = take(hk * tiles * kHeadDim * 4);
   w.part = take(hk * chunks * 2 * kMaxSink * kHeadDim * 4);
   w.sum = take(n_sink > 0 ? hk * 2 * kMaxSink * kHeadDim * 4 : 0);
