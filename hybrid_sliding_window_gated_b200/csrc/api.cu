@@ -975,28 +975,6 @@ int swa_global_decode_shared(const swa_params_t* p, int64_t prefix_len, int64_t 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
 
-  SharedPrepArgs pa{};
-  pa.N = static_cast<int>(p->B);
-  pa.Hq = p->Hq;
-  pa.Hkv = p->Hkv;
-  pa.G = G;
-  pa.half_rot = p->rot_dim / 2;
-  pa.rows_pad = w.rows_pad;
-  pa.eps = p->eps;
-  pa.base = prefix_len;
-  pa.cap = cache_cap;
-  pa.pos = pos;
-  pa.q = q;
-  pa.k = k_new;
-  pa.v = v_new;
-  pa.wq = wq;
-  pa.wk = wk;
-  pa.k_cache = k_cache;
-  pa.v_cache = v_cache;
-  pa.qs = reinterpret_cast<uint16_t*>(ws + w.qs);
-  pa.err = err;
-  fill_inv_freq(p, pa.inv_freq);
-
   PrefixArgs xa{};
   xa.Hkv = p->Hkv;
   xa.rows = static_cast<int>(p->B * G);
@@ -1035,7 +1013,13 @@ int swa_global_decode_shared(const swa_params_t* p, int64_t prefix_len, int64_t 
   a.rows_pad = w.rows_pad;
   a.pre_o = xa.part_o;
   a.pre_ml = xa.part_ml;
-  for (int j = 0; j < kMaxPairs; ++j) a.inv_freq[j] = pa.inv_freq[j];
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.wk = wk;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.qs = reinterpret_cast<uint16_t*>(ws + w.qs);
+  fill_inv_freq(p, a.inv_freq);
 
   // The prefix's tensor maps end at prefix_len: keys past it arrive as zeros.
   CUtensorMap tq, tkp, tvp, tk, tv;
@@ -1046,16 +1030,16 @@ int swa_global_decode_shared(const swa_params_t* p, int64_t prefix_len, int64_t 
                            CU_TENSOR_MAP_SWIZZLE_128B)))
     return rc;
   if (prefix_len > 0 &&
-      ((rc = encode_tmap_4d(&tq, pa.qs, D, w.rows_pad, p->Hkv, 2, 64, kTile, 1, 1,
+      ((rc = encode_tmap_4d(&tq, a.qs, D, w.rows_pad, p->Hkv, 2, 64, kTile, 1, 1,
                             CU_TENSOR_MAP_SWIZZLE_128B)) ||
        (rc = encode_tmap_4d(&tkp, k_prefix, D, prefix_len, p->Hkv, 1, 64, kTile, 1, 1,
                             CU_TENSOR_MAP_SWIZZLE_128B, false, prefix_cap)) ||
        (rc = encode_tmap_4d(&tvp, v_prefix, D, prefix_len, p->Hkv, 1, 64, kTile, 1, 1,
                             CU_TENSOR_MAP_SWIZZLE_128B, false, prefix_cap))))
     return rc;
-  if ((rc = launch_shared_prep(pa, st)) != SWA_OK) return rc;
+  if ((rc = launch_shared_own(tk, tv, a, st)) != SWA_OK) return rc;
   if (prefix_len > 0 && (rc = launch_prefix(tq, tkp, tvp, xa, st)) != SWA_OK) return rc;
-  return launch_shared_suffix(tk, tv, a, st);
+  return launch_shared_combine(a, st);
 }
 
 }  // extern "C"

@@ -647,6 +647,17 @@ __device__ __forceinline__ uint32_t ring_off(int s, int c) {
 // Barrier over the 128 consumer threads (named barrier 1).
 __device__ __forceinline__ void consumers_sync() { named_sync(1, 128); }
 
+// Zeros into n rows of a.qs from `row` on, of both terms.
+__device__ __forceinline__ void zero_rows(const GlobalDecArgs& a, long long row, long long n,
+                                          int tid) {
+  const long long half = static_cast<long long>(a.Hkv) * a.rows_pad * kHeadDim;
+  for (long long i = tid; i < n * (kHeadDim / 8); i += kDecThreads) {
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    *reinterpret_cast<uint4*>(a.qs + row * kHeadDim + 8 * i) = z;
+    *reinterpret_cast<uint4*>(a.qs + half + row * kHeadDim + 8 * i) = z;
+  }
+}
+
 // One CTA per (sequence, KV head, chunk of kGlobalChunk keys).  The chunk's
 // keys [c0, min(c0 + chunk, pos + 1)) arrive in tiles of 128 by TMA; warp w
 // scores keys 32 w .. 32 w + 31 of each tile with mma.sync (the group's query
@@ -654,7 +665,10 @@ __device__ __forceinline__ void consumers_sync() { named_sync(1, 128); }
 // partial O, and the four warps' partials are merged at the end into the
 // chunk's (max, sum, O) in the workspace.  kShared (a step behind a shared
 // prefix): the caches start at position a.base, and q' and P enter with a second
-// bf16 term each, in the M rows 8-15 that the group's heads leave empty.
+// bf16 term each, in the M rows 8-15 that the group's heads leave empty.  No other
+// kernel prepares that step: the first chunk's CTA also writes q' for the prefix's
+// kernel, and the CTA whose chunk takes the new token writes its k' and v to the
+// cache and into its own copy of the tile, whichever of the two the load has met.
 template <bool kShared>
 __global__ void __launch_bounds__(kDecThreads, 1)
     global_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -683,9 +697,18 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long long pa = a.pos[n], p = kShared ? pa - a.base : pa;  // position; its cache slot
   const long long c0 = static_cast<long long>(c) * kGlobalChunk;
-  if (p < 0 || p >= a.cap) {  // reported by the cache writer before this kernel
-    return;
+  const bool bad = p < 0 || p >= a.cap;
+  const long long q_at = static_cast<long long>(kvh) * a.rows_pad;  // rows of this head in a.qs
+  if (kShared && c == 0) {
+    // zeros for the rows that pad a head's to 128, and for a skipped sequence's
+    const long long pad0 = static_cast<long long>(a.N) * a.G, mine = static_cast<long long>(n) * a.G;
+    if (n == 0) zero_rows(a, q_at + pad0, a.rows_pad - pad0, tid);
+    if (bad) {
+      zero_rows(a, q_at + mine, a.G, tid);
+      if (kvh == 0 && tid == 0) atomicCAS(a.err, 0, kDevErrBadPosition);
+    }
   }
+  if (bad) return;  // (without a prefix reported by the cache writer before this kernel)
   if (c0 > p) return;  // the whole CTA: no key of this chunk is in the context
   const long long c1 = min(c0 + kGlobalChunk, p + 1);  // keys [c0, c1)
   const int ntile = static_cast<int>((c1 - c0 + kTile - 1) / kTile);
@@ -721,6 +744,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   }
   // ------------------------------------------------------------- consumers
   const int lw = warp - 1;
+  // the new token's slot, where this warp holds it (kShared)
+  const bool own_new = kShared && c1 == p + 1 && lw == (static_cast<int>(p - c0) & (kTile - 1)) >> 5;
+  uint2 k_row = make_uint2(0u, 0u), v_row = k_row;
   // q' for heads lw, lw + 4 at position p
   {
     float cs = 1.0f, sn = 0.0f;
@@ -733,10 +759,30 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       sm.qa[h][2 * lane] = h0;
       sm.qa[h][2 * lane + 1] = h1;
       if (kShared) {
-        sm.qa[kGlobalMaxGroup + h][2 * lane] = pack_bf16x2(x[0] - bf16_lo(h0), x[1] - bf16_hi(h0));
-        sm.qa[kGlobalMaxGroup + h][2 * lane + 1] =
-            pack_bf16x2(x[2] - bf16_lo(h1), x[3] - bf16_hi(h1));
+        const uint32_t r0 = pack_bf16x2(x[0] - bf16_lo(h0), x[1] - bf16_hi(h0));
+        const uint32_t r1 = pack_bf16x2(x[2] - bf16_lo(h1), x[3] - bf16_hi(h1));
+        sm.qa[kGlobalMaxGroup + h][2 * lane] = r0;
+        sm.qa[kGlobalMaxGroup + h][2 * lane + 1] = r1;
+        if (c == 0) {
+          uint16_t* dst =
+              a.qs + (q_at + static_cast<long long>(n) * a.G + h) * kHeadDim + 4 * lane;
+          *reinterpret_cast<uint2*>(dst) = make_uint2(h0, h1);
+          *reinterpret_cast<uint2*>(dst + static_cast<long long>(a.Hkv) * a.rows_pad * kHeadDim) =
+              make_uint2(r0, r1);
+        }
       }
+    }
+    if (own_new) {
+      const long long row = (static_cast<long long>(n) * a.Hkv + kvh) * kHeadDim + 4 * lane;
+      float x[4];
+      load4(a.k_new + row, x);
+      v_row = *reinterpret_cast<const uint2*>(a.v_new + row);
+      norm_rope_row(x, a.wk, a.eps, sm.scratch[lw], lane, a.half_rot, cs, sn);
+      k_row = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+      const long long at =
+          ((static_cast<long long>(n) * a.Hkv + kvh) * a.cap + p) * kHeadDim + 4 * lane;
+      *reinterpret_cast<uint2*>(a.k_cache + at) = k_row;
+      *reinterpret_cast<uint2*>(a.v_cache + at) = v_row;
     }
   }
   bool ok = true;
@@ -766,6 +812,12 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         for (int cc = 0; cc < 16; ++cc)
           *reinterpret_cast<uint4*>(&st.v[0][0] + ring_off(32 * lw + lane, cc)) = z;
         fence_proxy_async_smem();  // before a later TMA copy into this stage
+      }
+      if (own_new && i == ntile - 1) {  // the last tile: no copy into its stage follows
+        const int slot = static_cast<int>(p - key0);
+        const uint32_t off = ring_off(slot, lane >> 1) + (lane & 1) * 8;
+        *reinterpret_cast<uint2*>(&st.k[0][0] + off) = k_row;
+        *reinterpret_cast<uint2*>(&st.v[0][0] + off) = v_row;
       }
       __syncwarp();
     }
@@ -1006,8 +1058,8 @@ namespace swa {
 namespace glb {
 
 template <bool kShared>
-int launch_decode_impl(const CUtensorMap& tk, const CUtensorMap& tv, const GlobalDecArgs& a,
-                       cudaStream_t stream) {
+int launch_chunks(const CUtensorMap& tk, const CUtensorMap& tv, const GlobalDecArgs& a,
+                  cudaStream_t stream) {
   DeviceInfo di;
   int rc = current_device_info(&di);
   if (rc != SWA_OK) return rc;
@@ -1022,9 +1074,12 @@ int launch_decode_impl(const CUtensorMap& tk, const CUtensorMap& tv, const Globa
   }
   const long long items = static_cast<long long>(a.N) * a.Hkv * a.chunks;
   if (items > 0x7fffffffLL) return SWA_ERR_UNSUPPORTED;
-  rc = launch_dependent(global_decode_kernel<kShared>, static_cast<unsigned>(items), kDecThreads,
-                        smem, stream, tk, tv, a);
-  if (rc != SWA_OK) return rc;
+  return launch_dependent(global_decode_kernel<kShared>, static_cast<unsigned>(items), kDecThreads,
+                          smem, stream, tk, tv, a);
+}
+
+template <bool kShared>
+int launch_combine(const GlobalDecArgs& a, cudaStream_t stream) {
   const long long rows = static_cast<long long>(a.N) * a.Hq;
   return launch_dependent(global_combine_kernel<kShared>, static_cast<unsigned>((rows + 7) / 8),
                           256, 0, stream, a);
@@ -1034,12 +1089,17 @@ int launch_decode_impl(const CUtensorMap& tk, const CUtensorMap& tv, const Globa
 
 int launch_global_decode(const CUtensorMap& tk, const CUtensorMap& tv, const GlobalDecArgs& a,
                          cudaStream_t stream) {
-  return glb::launch_decode_impl<false>(tk, tv, a, stream);
+  const int rc = glb::launch_chunks<false>(tk, tv, a, stream);
+  return rc != SWA_OK ? rc : glb::launch_combine<false>(a, stream);
 }
 
-int launch_shared_suffix(const CUtensorMap& tk, const CUtensorMap& tv, const GlobalDecArgs& a,
-                         cudaStream_t stream) {
-  return glb::launch_decode_impl<true>(tk, tv, a, stream);
+int launch_shared_own(const CUtensorMap& tk, const CUtensorMap& tv, const GlobalDecArgs& a,
+                      cudaStream_t stream) {
+  return glb::launch_chunks<true>(tk, tv, a, stream);
+}
+
+int launch_shared_combine(const GlobalDecArgs& a, cudaStream_t stream) {
+  return glb::launch_combine<true>(a, stream);
 }
 
 }  // namespace swa

@@ -66,27 +66,12 @@ struct GlobalDecArgs {
   int rows_pad;           // query rows per KV head, rounded up to 128
   const float* pre_o;     // [Hkv, splits, rows_pad, D] fp32
   const float* pre_ml;    // [Hkv, splits, rows_pad, 2] fp32
-  double inv_freq[kMaxPairs];
-};
-
-// The new tokens of a shared-prefix step: k', v into the sequences' caches, and
-// q' into the workspace as the bf16 of its value and of what that left over.
-struct SharedPrepArgs {
-  int N, Hq, Hkv, G;
-  int half_rot;
-  int rows_pad;
-  float eps;
-  long long base, cap;
-  const int64_t* pos;
-  const uint16_t* q;
-  const uint16_t* k;
-  const uint16_t* v;
-  const float* wq;
+  const uint16_t* k_new;  // [N, Hkv, D]
+  const uint16_t* v_new;
   const float* wk;
-  uint16_t* k_cache;
+  uint16_t* k_cache;      // [N, Hkv, cap, D]
   uint16_t* v_cache;
-  uint16_t* qs;           // [2, Hkv, rows_pad, D]: value, remainder
-  int* err;
+  uint16_t* qs;           // [2, Hkv, rows_pad, D]: q' as bf16, and what that left over
   double inv_freq[kMaxPairs];
 };
 
@@ -112,11 +97,11 @@ struct SharedWs {
 };
 SharedWs shared_ws(long long N, int Hkv, int G, long long prefix, long long cap);
 
-int launch_shared_prep(const SharedPrepArgs& a, cudaStream_t stream);
 int launch_prefix(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                   const PrefixArgs& a, cudaStream_t stream);
-int launch_shared_suffix(const CUtensorMap& tk, const CUtensorMap& tv, const GlobalDecArgs& a,
-                         cudaStream_t stream);
+int launch_shared_own(const CUtensorMap& tk, const CUtensorMap& tv, const GlobalDecArgs& a,
+                      cudaStream_t stream);
+int launch_shared_combine(const GlobalDecArgs& a, cudaStream_t stream);
 
 inline size_t global_decode_ws_bytes(long long N, int Hkv, int G, long long cap) {
   const long long chunks = (cap + kGlobalChunk - 1) / kGlobalChunk;

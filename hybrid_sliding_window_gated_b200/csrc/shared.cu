@@ -4,12 +4,12 @@
 //   o_n = softmax over [prefix keys 0 .. L-1 ; own keys L .. pos_n] of q'_n . k'
 //
 // Split at the prefix's end, the two parts are separate softmaxes joined by
-// their maxima and sums.  Four kernels:
-//   shared_prep_kernel    k' and v of the new tokens into the sequences' caches;
-//                         q' of all of them into the workspace.
+// their maxima and sums.  Three kernels:
+//   global_decode_kernel  (global.cu) the sequences' own keys, split over chunks; it
+//                         also writes the new tokens' k' and v to the caches and q'
+//                         to the workspace.
 //   prefix_attn_kernel    (here) the prefix part.
-//   global_decode_kernel, global_combine_kernel (global.cu) the sequences' own
-//                         keys, split over chunks, and the join.
+//   global_combine_kernel (global.cu) the join.
 //
 // The prefix part.  For one KV head the N G query rows are a matrix Q' (rows x
 // 128) against K' and V (L x 128): 4 x 128 operations per row and key, 512 bytes
@@ -33,11 +33,9 @@
 // which bf16 and fp32 hold without loss).
 #include <atomic>
 
-#include "decode_internal.h"
 #include "global_internal.h"
 #include "launch.cuh"
 #include "ptx.cuh"
-#include "rowops.cuh"
 
 namespace swa {
 namespace shr {
@@ -382,61 +380,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// One warp per (sequence, head): q' of a query head into the workspace as two
-// bf16 terms, k' and v of a KV head into slot pos - base of the sequence's cache.
-// Further warps zero the workspace rows that pad a KV head's rows to 128.
-__global__ void __launch_bounds__(256) shared_prep_kernel(const SharedPrepArgs a) {
-  __shared__ __align__(16) float scratch[8][kHeadDim];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long w = static_cast<long long>(blockIdx.x) * 8 + warp;
-  const int per = a.Hq + a.Hkv;
-  const long long half = static_cast<long long>(a.Hkv) * a.rows_pad * kHeadDim;
-  const long long rows = static_cast<long long>(a.N) * a.G;
-  const uint2 z = make_uint2(0u, 0u);
-  if (w >= static_cast<long long>(a.N) * per) {
-    const long long x = w - static_cast<long long>(a.N) * per, pad = a.rows_pad - rows;
-    if (pad == 0 || x >= pad * a.Hkv) return;
-    const long long at = ((x / pad) * a.rows_pad + rows + x % pad) * kHeadDim + 4 * lane;
-    *reinterpret_cast<uint2*>(a.qs + at) = z;
-    *reinterpret_cast<uint2*>(a.qs + half + at) = z;
-    return;
-  }
-  const long long n = w / per;
-  const int h = static_cast<int>(w - n * per);
-  const long long pos = a.pos[n], slot = pos - a.base;
-  const bool bad = pos < a.base || slot >= a.cap;
-  if (bad && h == 0 && lane == 0) atomicCAS(a.err, 0, kDevErrBadPosition);
-  float cs = 1.0f, sn = 0.0f;
-  if (!bad && lane < a.half_rot)
-    rope_cos_sin(static_cast<double>(pos), a.inv_freq[lane], &cs, &sn);
-  float x[4];
-  if (h < a.Hq) {
-    const int kvh = h / a.G;
-    const long long at = (kvh * static_cast<long long>(a.rows_pad) + n * a.G + (h - kvh * a.G)) *
-                             kHeadDim + 4 * lane;
-    load4(a.q + (n * a.Hq + h) * kHeadDim + 4 * lane, x);
-    norm_rope_row(x, a.wq, a.eps, scratch[warp], lane, a.half_rot, cs, sn);
-    uint2 hi = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-    uint2 lo = make_uint2(pack_bf16x2(x[0] - bf16_lo(hi.x), x[1] - bf16_hi(hi.x)),
-                          pack_bf16x2(x[2] - bf16_lo(hi.y), x[3] - bf16_hi(hi.y)));
-    if (bad) hi = lo = z;
-    *reinterpret_cast<uint2*>(a.qs + at) = hi;
-    *reinterpret_cast<uint2*>(a.qs + half + at) = lo;
-  } else if (!bad) {
-    const int kvh = h - a.Hq;
-    const long long row = (n * a.Hkv + kvh) * kHeadDim + 4 * lane;
-    load4(a.k + row, x);
-    const uint2 vv = *reinterpret_cast<const uint2*>(a.v + row);
-    norm_rope_row(x, a.wk, a.eps, scratch[warp], lane, a.half_rot, cs, sn);
-    const long long at = ((n * a.Hkv + kvh) * a.cap + slot) * kHeadDim + 4 * lane;
-    *reinterpret_cast<uint2*>(a.k_cache + at) =
-        make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-    *reinterpret_cast<uint2*>(a.v_cache + at) = vv;
-  }
-}
-
 }  // namespace shr
 
 // The split of the prefix over CTAs: the count per KV head (and row pair) whose
@@ -474,14 +417,6 @@ SharedWs shared_ws(long long N, int Hkv, int G, long long prefix, long long cap)
   w.part_ml = w.part_o + up(own_rows * kHeadDim * 4);
   w.total = w.part_ml + up(own_rows * 8);
   return w;
-}
-
-int launch_shared_prep(const SharedPrepArgs& a, cudaStream_t stream) {
-  const long long warps = static_cast<long long>(a.N) * (a.Hq + a.Hkv) +
-                          (a.rows_pad - static_cast<long long>(a.N) * a.G) * a.Hkv;
-  const long long grid = (warps + 7) / 8;
-  if (grid > 0x7fffffffLL) return SWA_ERR_UNSUPPORTED;
-  return launch_dependent(shr::shared_prep_kernel, static_cast<unsigned>(grid), 256, 0, stream, a);
 }
 
 int launch_prefix(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
