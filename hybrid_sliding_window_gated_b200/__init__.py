@@ -162,6 +162,13 @@ def _need(where, device, **tensors):
                              f"the device of the first input")
 
 
+def _on_current_device(where, device):
+    """The library launches on the current device, whatever device the tensors are on."""
+    if device.type == "cuda" and device.index != torch.cuda.current_device():
+        raise ValueError(f"{where}: the tensors are on {device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
 def make_params(B, T, Hq, Hkv, *, head_dim=128, window=128, rot_dim=42, rope_base=1e4, eps=1e-6,
                 scale=0.0, flags=0):
     return Params(B, T, Hq, Hkv, head_dim, window, rot_dim, flags, rope_base, eps, scale)
@@ -522,6 +529,7 @@ def sink_fwd(q, k, v, g, wq, wk, n_sink, *, window=128, rot_dim=42, rope_base=1e
     nq, nk = B * T * Hq * D, B * T * Hkv * D
     bf, f32 = torch.bfloat16, torch.float32
     opt = {} if lse is None else {"lse": (lse, f32, B * Hq * T)}
+    _on_current_device("swa_sink_fwd", q.device)
     _need("swa_sink_fwd", q.device, q=(q, bf, nq), k=(k, bf, nk), v=(v, bf, nk), g=(g, bf, nq),
           wq=(wq, f32, D if nq else 0), wk=(wk, f32, D if nq else 0), out=(out, bf, nq), **opt)
     rc = lib().swa_sink_fwd(ctypes.byref(p), n_sink, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(wq),
@@ -551,6 +559,7 @@ def sink_bwd(q, k, v, g, wq, wk, o, lse, dO, n_sink, *, window=128, rot_dim=42, 
     nbytes = int(lib().swa_sink_bwd_workspace_size(ctypes.byref(p), n_sink))
     if workspace is None:
         workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
+    _on_current_device("swa_sink_bwd", q.device)
     _need_bwd("swa_sink_bwd", q, k, v, g, wq, wk, lse, dO, grads,
               o=(o, torch.bfloat16, B * T * Hq * D), workspace=(workspace, torch.uint8, nbytes))
     rc = lib().swa_sink_bwd(ctypes.byref(p), n_sink, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(wq),
@@ -575,6 +584,7 @@ def sink_decode_step(pos, q, k_new, v_new, g, wq, wk, k_cache, v_cache, k_sink, 
                     eps=eps, scale=scale, flags=flags)
     nq, nk = N * Hq * D, N * Hkv * D
     bf, f32 = torch.bfloat16, torch.float32
+    _on_current_device("swa_sink_decode_step", q.device)
     _need("swa_sink_decode_step", q.device, pos=(pos, torch.int64, N), q=(q, bf, nq),
           k_new=(k_new, bf, nk), v_new=(v_new, bf, nk), g=(g, bf, nq),
           wq=(wq, f32, D if N else 0), wk=(wk, f32, D if N else 0),
@@ -601,6 +611,7 @@ def prefill_to_sinks(k, v, wk, k_sink, v_sink, starts=None, lens=None, pos0=None
     nk = (B if lens is None else 1) * T * Hkv * D if n else 0
     extra = {name: (t, i64, B) for name, t in (("starts", starts), ("lens", lens), ("pos0", pos0))
              if t is not None}
+    _on_current_device("swa_prefill_to_sinks", k_sink.device)
     _need("swa_prefill_to_sinks", k_sink.device, k=(k, bf, nk), v=(v, bf, nk),
           wk=(wk, torch.float32, D if n else 0), k_sink=(k_sink, bf, n), v_sink=(v_sink, bf, n),
           **extra)
@@ -638,6 +649,7 @@ def global_decode_shared(pos, q, k_new, v_new, wq, wk, k_prefix, v_prefix, prefi
     nq, nk = N * Hq * D, N * Hkv * D
     npre = Hkv * pcap * D if N and prefix_len else 0
     bf, f32 = torch.bfloat16, torch.float32
+    _on_current_device("swa_global_decode_shared", q.device)
     _need("swa_global_decode_shared", q.device, pos=(pos, torch.int64, N), q=(q, bf, nq),
           k_new=(k_new, bf, nk), v_new=(v_new, bf, nk), wq=(wq, f32, D if N else 0),
           wk=(wk, f32, D if N else 0), k_prefix=(k_prefix, bf, npre), v_prefix=(v_prefix, bf, npre),

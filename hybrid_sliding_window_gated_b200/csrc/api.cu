@@ -734,7 +734,8 @@ int swa_sink_fwd(const swa_params_t* p, int32_t n_sink, const swa_bf16_t* q, con
   a.tiles = static_cast<int>((p->T + kSinkTile - 1) / kSinkTile);
   if (p->B * p->Hkv > 0x7fffffffll) return SWA_ERR_UNSUPPORTED;  // chains are counted in 32 bits
   a.total_tiles = static_cast<long long>(a.tiles) * p->B * p->Hkv;
-  if (a.total_tiles > (1ll << 24)) return SWA_ERR_UNSUPPORTED;  // a CTA's jobs are counted in 32 bits
+  // a CTA counts its units (tiles x head pairs) in 32 bits
+  if (a.total_tiles > (1ll << 24)) return SWA_ERR_UNSUPPORTED;
   a.scale_log2 = score_scale(p) * 1.4426950408889634f;
   a.eps = p->eps;
   a.flags = p->flags;

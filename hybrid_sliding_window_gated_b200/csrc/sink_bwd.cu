@@ -21,7 +21,7 @@
 //   sink_bwd_q_kernel     query-major: 16 queries of one head per warp step, nine
 //                         band blocks and the sinks: S, dP, D, dQ.  Writes dq and D.
 //   sink_bwd_sink_kernel  the sinks' dk' and dv: every query contributes to the same
-//                         16 keys, so chunks of 512 tokens make partial sums, and
+//                         16 keys, so chunks of tokens make partial sums, and
 //   sink_bwd_sum_kernel   adds them up in a fixed order.
 //   sink_bwd_k_kernel     key-major: 16 keys per warp against the nine blocks of
 //                         queries that see them, all heads of the group: S^T, dP^T,
@@ -29,11 +29,17 @@
 //   sink_bwd_w_kernel     adds up the CTAs' dwq and dwk in a fixed order.
 // No sum is made by atomics, so results do not depend on the order of CTAs.
 //
-// What bounds it: the seven products of 160 keys per query on mma.sync (see
-// sink_fwd.cu on why not tcgen05), 39 us each for 16,384 tokens of 32 heads at
-// 550 TFLOP/s, with as many shared-memory cycles for their operands; memory
-// needs about 0.19 ms.  The two passes instead of one with atomics cost two
-// products; a band keeps dK and dV of 192 keys live, too many for registers.
+// What bounds it.  The seven products of 160 keys per query take 39 us each for
+// 16,384 tokens of 32 / 8 heads at the 550 TFLOP/s that mma.sync reaches, with about
+// as many shared-memory cycles for their operands; memory needs 0.19 ms.  Warp tiles
+// of 16 x 16 waste little of the 128-key band (1.1 of 1), where tcgen05's 128 rows
+// of two heads would compute 1.6 times the products and hand S, dP, P and dS through
+// TMEM; the two passes instead of one with atomics cost two products, since a band
+// keeps dK and dV of 192 keys live, too many for registers.
+//
+// Measured there (us): kv 41, rows 190, q 350, sinks 62 + 5, k 334, w 6; the
+// key-major pass reads its operands from shared memory at 66 % of the pipe's rate
+// with the tensor pipe at 44 %, and the query-major pass is its S - P - dS chain.
 //
 // Numbers.  All products have fp16 operands and fp32 sums.  q' and k' are divided
 // by a power of two not below the norm weights (at most sqrt(128) then); a row

@@ -1,6 +1,6 @@
-// sink_common.cuh -- what the sink-attention kernels share: fp16 / bf16 warp
-// MMAs, the order in which a row's 128 dims lie in shared memory, and the
-// K' / V tile producer.
+// sink_common.cuh -- what the sink-attention kernels share, most of it the
+// backward's: fp16 warp MMAs, the order in which a row's 128 dims lie in its
+// operand tiles, rows' scales, and the gate's two sigmoids.
 //
 // Order of the dims.  A contraction over the 128 dims may run over them in any
 // order as long as both operands use the same one, and the columns of a product
@@ -30,7 +30,7 @@ constexpr int kTileBytes = kSinkTile * kRowBytes;   // 16 KiB
 constexpr int kSinkBytes = kMaxSink * kRowBytes;    // 4 KiB
 constexpr int kRopeDims = 2 * kMaxPairs;            // dims 0..47 hold every rotated pair
 
-// D (16x8 fp32) += A (16x16) * B (16x8), fp16 and bf16.  Not volatile: a pure
+// D (16x8 fp32) += A (16x16) * B (16x8), fp16.  Not volatile: a pure
 // function of registers, which the compiler may move between other work.
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
@@ -39,14 +39,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
-      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -75,16 +67,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool r
   const int n = real ? 16 : 0;  // 0: the 16 bytes are filled with zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
                : "memory");
-}
-__device__ __forceinline__ void st_shared4(uint32_t at, const uint32_t* x) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]), "r"(x[1]),
-               "r"(x[2]), "r"(x[3])
-               : "memory");
-}
-__device__ __forceinline__ void ld_shared4(uint32_t at, uint32_t (&x)[4]) {
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-               : "r"(at));
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -138,8 +120,7 @@ __device__ __forceinline__ void rest_pos(int lane, int* chunk0, int* byte) {
   }
 }
 
-// k' / ck of N rows, fp16, in rope order into rows r0 .. of `tile` (row_at(e) is the
-// row e is swizzled as); w_* are this lane's weights divided by ck, rot its pair's
+// k' / ck of N rows, fp16, in rope order into rows r0 .. of `tile`; w_* are this lane's weights divided by ck, rot its pair's
 // rotation at each row's position.  The rows' chains of shuffles run side by side.
 template <int N>
 __device__ __forceinline__ void store_k_rows(uint8_t* tile, int r0, const KRow (&x)[N], int lane,
@@ -249,35 +230,11 @@ __device__ __forceinline__ void pdl_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// The raw row of x that a fragment's thread c covers: pairs 8 kk + 2 c + e and
+// The raw row of x as floats, as far as a fragment's thread c covers it: pairs 8 kk + 2 c + e and
 // dims 48 + 4 c .., 64 + 8 c .., 96 + 8 c ...
 struct RawRow {
   float lo[6], hi[6], rest[20];
 };
-__device__ __forceinline__ void load_raw(RawRow& x, const uint16_t* row, int c, int P) {
-  if (row == nullptr) {
-#pragma unroll
-    for (int i = 0; i < 6; ++i) x.lo[i] = x.hi[i] = 0.f;
-#pragma unroll
-    for (int i = 0; i < 20; ++i) x.rest[i] = 0.f;
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 6; ++i) {
-    const int j = 8 * (i >> 1) + 2 * c + (i & 1);
-    x.lo[i] = bf16_f32(__ldg(row + pair_lo(j, P)));
-    x.hi[i] = bf16_f32(__ldg(row + pair_hi(j, P)));
-  }
-  const uint2 r3 = __ldg(reinterpret_cast<const uint2*>(row + 48 + 4 * c));
-  const uint4 r4 = __ldg(reinterpret_cast<const uint4*>(row + 64 + 8 * c));
-  const uint4 r6 = __ldg(reinterpret_cast<const uint4*>(row + 96 + 8 * c));
-  const uint32_t w[10] = {r3.x, r3.y, r4.x, r4.y, r4.z, r4.w, r6.x, r6.y, r6.z, r6.w};
-#pragma unroll
-  for (int i = 0; i < 10; ++i) {
-    x.rest[2 * i] = bf16_lo(w[i]);
-    x.rest[2 * i + 1] = bf16_hi(w[i]);
-  }
-}
 // Dim of rest[i] (thread c), and its weight.
 __device__ __forceinline__ int rest_dim(int i, int c) {
   return i < 4 ? 48 + 4 * c + i : (i < 12 ? 64 + 8 * c + (i - 4) : 96 + 8 * c + (i - 12));
@@ -292,7 +249,6 @@ __device__ __forceinline__ float raw_rinv(const RawRow& x, float eps) {
   s += __shfl_xor_sync(0xffffffffu, s, 2);
   return rsqrtf(s * (1.0f / kHeadDim) + eps);
 }
-
 
 }  // namespace snk
 }  // namespace swa

@@ -804,18 +804,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // P is 2^14 at the row's maximum, so that fp16 keeps P down to 2^-28 of it normal.
       const float ms = mx == -INFINITY ? 0.0f : mx * sc - 14.0f;  // all NaN: any reference
-      // Least exponent of the V rows at hand; almost always no row is scaled.
+      // Least exponent of the V rows that this row sees (what a masked one holds must
+      // not matter).  With V near 1 no row is scaled.
       bool scaled = see_sinks && sm.scaled[kSlots] != 0;
       for (int s = 0; s < kSlots; ++s) scaled = scaled || (dist(s) >= 0 && sm.scaled[s] != 0);
       float am = 0.0f;
       if (scaled) {
         am = 126.0f;
-        for (int s = 0; s < kSlots; ++s)
-          if (dist(s) >= 0)
-            am = fminf(am, fminf(sm.va[s * kTok + lane], sm.va[s * kTok + 32 + lane]));
-        if (see_sinks && lane < a.n_sink) am = fminf(am, sm.va[kSlots * kTok + lane]);
+#pragma unroll 1
+        for (int s = 0; s < kSlots; ++s) {
+          const int d = dist(s);
+          if (d < 0) continue;
+#pragma unroll 4
+          for (int j = 0; j < kTok; j += 4) {
+            const float4 e = *reinterpret_cast<const float4*>(&sm.va[s * kTok + j]);
+            const float ev[4] = {e.x, e.y, e.z, e.w};
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) am = fminf(am, __shfl_xor_sync(0xffffffffu, am, o));
+            for (int i = 0; i < 4; ++i)
+              if (d == 0 ? j + i <= tok : (d == 1 || j + i > tok)) am = fminf(am, ev[i]);
+          }
+        }
+        if (see_sinks)
+          for (int i = 0; i < kMaxSink; ++i)
+            if (i <= sink_hi) am = fminf(am, sm.va[kSlots * kTok + i]);
+        __syncwarp();
       }
       // P = 2^(s sc - ms) as fp16 over the region's first columns, slot by slot: P of
       // slot s goes to columns 32 s .., which slots 0 .. s have been read out of.

@@ -71,9 +71,11 @@ enum {
 };
 
 /* Debug bits for swa_params_t.flags (0 in normal use).  FORCE_TIMEOUT makes
- * the kernels of swa_fwd, swa_bwd and swa_decode_step wait on a barrier that
- * nothing completes, so tests can check that the bounded wait ends the kernel
- * (its copies drained, TMEM freed) and reports SWA_ERR_DEVICE_TIMEOUT. */
+ * the kernels of swa_fwd, swa_bwd, swa_decode_step, swa_sink_fwd,
+ * swa_sink_decode_step and of swa_global_decode_shared's prefix part wait on a
+ * barrier that nothing completes, so tests can check that the bounded wait ends
+ * the kernel (its copies drained, TMEM freed) and reports
+ * SWA_ERR_DEVICE_TIMEOUT. */
 enum { SWA_FLAG_FORCE_TIMEOUT = 1 };
 
 typedef struct swa_params {
@@ -345,9 +347,11 @@ int swa_sink_fwd(const swa_params_t* p, int32_t n_sink, const swa_bf16_t* q, con
  * the upstream gradient dO.  Writes dq, dk, dv, dg (bf16) and ADDS the weight
  * gradients into dwq, dwk [D] (fp32; the caller zeroes them).  Sums are made in a
  * fixed order: equal inputs give equal bits.  Gradients and values of any finite
- * magnitude are carried (per-row power-of-two scales); inputs that are not finite
- * reach the gradients of the tokens around them.  `workspace`: caller-owned device
- * scratch of swa_sink_bwd_workspace_size bytes, 256-byte aligned.  Pointers 16-byte
+ * magnitude are carried by power-of-two scales per row; where an index is summed over,
+ * entries 2^24 below the largest among the 192 tokens at hand lose bits, so rows
+ * behind a padded sequence should hold numbers of ordinary size (and dO = 0): infinities
+ * and NaN reach the gradients of the tokens around them.  `workspace`: caller-owned
+ * device scratch of swa_sink_bwd_workspace_size bytes, 256-byte aligned.  Pointers 16-byte
  * aligned; errors as swa_fwd.
  */
 int swa_sink_bwd(const swa_params_t* p, int32_t n_sink, const swa_bf16_t* q, const swa_bf16_t* k,

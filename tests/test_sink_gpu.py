@@ -135,6 +135,23 @@ def test_values_that_are_not_finite_reach_only_rows_that_see_them(bad):
     assert su.rel(o[~hit], o_ref[~hit]) <= REL
 
 
+@pytest.mark.parametrize("size", [1.0, 1e-3, 1e-20])
+def test_huge_values_in_masked_places(size):
+    """Keys that a row does not see leave its V rows' scale alone: later tokens, and
+    those that the window has left behind."""
+    x = su.draw(1, 400, 4, 2, seed=71)
+    x["v"] = (x["v"].float() * size).to(torch.bfloat16)
+    clean = {n: t.clone() for n, t in x.items()}
+    x["v"][0, 100] = 3e38
+    x["v"][0, 333:] = -3e38
+    rows = torch.tensor([i for i in range(333) if i < 100 or i >= 228])
+    o, _ = forward(x, 3)
+    o_ref, _ = su.sink_forward(*su.args(clean, dtype=torch.float64), 3, 42, 1e4)
+    assert torch.isfinite(o).all()
+    d = (o.double().cpu() - o_ref)[:, rows].norm(dim=-1)
+    assert (d <= 2 * REL * o_ref[:, rows].norm(dim=-1)).all()
+
+
 def test_gate_at_infinity():
     x = su.draw(1, 200, 2, 1, seed=12)
     x["g"][0, :, 0] = -float("inf")

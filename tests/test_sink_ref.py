@@ -185,3 +185,10 @@ def test_binding_refuses_wrong_tensors(L):
     with pytest.raises(ValueError, match="more than one"):
         swa.global_decode_shared(torch.zeros(1, dtype=torch.int64), x["q"][:, 0], x["k"][:, 0],
                                  x["v"][:, 0], x["wq"], x["wk"], z, z, 16, z[:1], z[:1])
+
+
+def test_tensors_on_another_device_refused(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    swa._on_current_device("f", torch.device("cuda", 1))
+    with pytest.raises(ValueError, match="current device is cuda:1"):
+        swa._on_current_device("f", torch.device("cuda", 0))
