@@ -37,7 +37,7 @@
 // TMEM; the two passes instead of one with atomics cost two products, since a band
 // keeps dK and dV of 192 keys live, too many for registers.
 //
-// Measured there (us): kv 41, rows 190, q 350, sinks 62 + 5, k 334, w 6; the
+// Measured there (us): kv 41, rows 170, q 350, sinks 62 + 5, k 334, w 6; the
 // key-major pass reads its operands from shared memory at 66 % of the pipe's rate
 // with the tensor pipe at 44 %, and the query-major pass is its S - P - dS chain.
 //
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(256) sink_bwd_kv_kernel(const SinkBwdArgs a) {
 // One warp per 16 tokens of a query head, two rows at a time and four dims per lane:
 // q' and dA as operand rows, dg, and the rows' lse and exponent b.  Bound by memory:
 // 1 KiB read and 768 bytes written per row.  The next two rows are on their way to
-// shared memory while a pair is worked on (190 us for 16,384 tokens of 32 heads,
+// shared memory while a pair is worked on (170 us for 16,384 tokens of 32 heads,
 // 241 with plain loads and as many warps).
 __global__ void __launch_bounds__(256, 4) sink_bwd_rows_kernel(const SinkBwdArgs a) {
   constexpr int kN = 2;

@@ -205,11 +205,17 @@ __device__ __forceinline__ float v_exp(float m) {
 
 // sigmoid(g) and 1 - sigmoid(g) = sigmoid(-g) of two values, each with its own
 // relative accuracy: with e = exp(-|g|) and r = 1 / (1 + e) they are r and e r, or
-// the other way round (the evaluation of sigmoid2, kept to both halves).
+// the other way round (the evaluation of sigmoid2, kept to both halves; with a
+// reciprocal instruction per value instead the backward's rows take 190 us, not 170).
 __device__ __forceinline__ float2 sigmoid_both(float2 g, float2* rest) {
   constexpr float kL2e = 1.4426950408889634f;
   const float2 e = make_float2(ex2_approx(-fabsf(g.x) * kL2e), ex2_approx(-fabsf(g.y) * kL2e));
-  const float2 r = make_float2(__frcp_rn(1.0f + e.x), __frcp_rn(1.0f + e.y));
+  const float2 d = __fadd2_rn(e, make_float2(1.0f, 1.0f));
+  float2 r = __ffma2_rn(d, make_float2(0.32286211f, 0.32286211f),
+                        make_float2(-1.45351115f, -1.45351115f));
+  r = __ffma2_rn(r, d, make_float2(2.12052006f, 2.12052006f));
+  const float2 t = __ffma2_rn(make_float2(-d.x, -d.y), r, make_float2(1.0f, 1.0f));
+  r = __ffma2_rn(r, t, r);
   const float2 er = __fmul2_rn(e, r);
   *rest = make_float2(g.x >= 0.0f ? er.x : r.x, g.y >= 0.0f ? er.y : r.y);
   return make_float2(g.x >= 0.0f ? r.x : er.x, g.y >= 0.0f ? r.y : er.y);
