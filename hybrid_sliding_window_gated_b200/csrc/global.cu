@@ -961,44 +961,61 @@ __global__ void __launch_bounds__(256) global_combine_kernel(const GlobalDecArgs
   if (r >= static_cast<long long>(a.N) * a.Hq) return;
   const int n = static_cast<int>(r / a.Hq), hq = static_cast<int>(r % a.Hq);
   const int kvh = hq / a.G, h = hq - kvh * a.G;
+  const long long pre = kShared ? static_cast<long long>(kvh) * a.splits * a.rows_pad +
+                                      static_cast<long long>(n) * a.G + h
+                                : 0;
+  const int splits = kShared ? a.splits : 0;
+  // Partials 32 at a time: a lane holds one's maximum and sum, so that their loads and
+  // those of the O rows overlap.  The sums run in the partials' order.
+  const auto ml_of = [&](int c, int count, const float* ml, long long first, long long step) {
+    return c < count ? *reinterpret_cast<const float2*>(ml + (first + c * step) * 2)
+                     : make_float2(-INFINITY, 0.0f);
+  };
+  float2 pre_x = ml_of(lane, splits, a.pre_ml, pre, a.rows_pad);
   const long long p = kShared ? a.pos[n] - a.base : a.pos[n];
   if (p < 0 || p >= a.cap) return;
   const int nc = static_cast<int>(p / kGlobalChunk) + 1;
   const long long base = (static_cast<long long>(n) * a.Hkv + kvh) * a.chunks;
-  float mx = -INFINITY;
-  for (int c = 0; c < nc; ++c) mx = fmaxf(mx, a.part_ml[((base + c) * a.G + h) * 2]);
-  const long long pre = kShared ? static_cast<long long>(kvh) * a.splits * a.rows_pad +
-                                      static_cast<long long>(n) * a.G + h
-                                : 0;
-  if (kShared)
-    for (int c = 0; c < a.splits; ++c)
-      mx = fmaxf(mx, a.pre_ml[(pre + static_cast<long long>(c) * a.rows_pad) * 2]);
+  float2 own_x = ml_of(lane, nc, a.part_ml, base * a.G + h, a.G);
+  float mx = fmaxf(own_x.x, pre_x.x);
+  for (int c = lane + 32; c < nc; c += 32)
+    mx = fmaxf(mx, ml_of(c, nc, a.part_ml, base * a.G + h, a.G).x);
+  for (int c = lane + 32; c < splits; c += 32)
+    mx = fmaxf(mx, ml_of(c, splits, a.pre_ml, pre, a.rows_pad).x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   float y[4] = {0.f, 0.f, 0.f, 0.f}, lsum = 0.0f;
-  for (int c = 0; c < nc; ++c) {
-    const long long slot = (base + c) * a.G + h;
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + slot * 2);
-    const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - mx);
-    lsum += f * ml.y;
-    const float4 v4 = *reinterpret_cast<const float4*>(a.part_o + slot * kHeadDim + 4 * lane);
-    y[0] += f * v4.x;
-    y[1] += f * v4.y;
-    y[2] += f * v4.z;
-    y[3] += f * v4.w;
-  }
-  if (kShared) {
-    for (int c = 0; c < a.splits; ++c) {
-      const long long slot = pre + static_cast<long long>(c) * a.rows_pad;
-      const float2 ml = *reinterpret_cast<const float2*>(a.pre_ml + slot * 2);
-      if (ml.x == -INFINITY) continue;  // a split without keys: its O was not written
-      const float f = ex2_approx(ml.x - mx);
-      lsum += f * ml.y;
-      const float4 v4 = *reinterpret_cast<const float4*>(a.pre_o + slot * kHeadDim + 4 * lane);
-      y[0] += f * v4.x;
-      y[1] += f * v4.y;
-      y[2] += f * v4.z;
-      y[3] += f * v4.w;
+  const auto join = [&](float2 x, int count, const float* ml, const float* part, long long first,
+                        long long step) {
+    for (int c0 = 0; c0 < count; c0 += 32) {
+      if (c0 > 0) x = ml_of(c0 + lane, count, ml, first, step);
+      const float fl = x.x == -INFINITY ? -1.0f : ex2_approx(x.x - mx);
+      for (int j0 = 0; j0 < min(32, count - c0); j0 += 8) {
+        float4 v4[8];
+        float f[8], l[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          f[e] = __shfl_sync(0xffffffffu, fl, j0 + e);
+          l[e] = __shfl_sync(0xffffffffu, x.y, j0 + e);
+          v4[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (!(f[e] < 0.0f))  // else no such partial, or one without keys whose O was not written
+            v4[e] = __ldg(reinterpret_cast<const float4*>(
+                part + (first + (c0 + j0 + e) * step) * kHeadDim + 4 * lane));
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float w = f[e] < 0.0f ? 0.0f : f[e];
+          lsum += w * l[e];
+          y[0] += w * v4[e].x;
+          y[1] += w * v4[e].y;
+          y[2] += w * v4[e].z;
+          y[3] += w * v4[e].w;
+        }
+      }
     }
-  }
+  };
+  join(own_x, nc, a.part_ml, a.part_o, base * a.G + h, a.G);
+  if (kShared) join(pre_x, splits, a.pre_ml, a.pre_o, pre, a.rows_pad);
   const float il = 1.0f / lsum;
   *reinterpret_cast<uint2*>(a.o + r * kHeadDim + 4 * lane) =
       make_uint2(pack_bf16x2(y[0] * il, y[1] * il), pack_bf16x2(y[2] * il, y[3] * il));
