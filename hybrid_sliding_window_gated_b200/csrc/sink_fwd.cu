@@ -808,6 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // not matter).  With V near 1 no row is scaled.
       bool scaled = see_sinks && sm.scaled[kSlots] != 0;
       for (int s = 0; s < kSlots; ++s) scaled = scaled || (dist(s) >= 0 && sm.scaled[s] != 0);
+      scaled = __any_sync(0xffffffffu, scaled);  // TMEM loads below: one way for the warp
       float am = 0.0f;
       if (scaled) {
         am = 126.0f;
@@ -917,6 +918,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // V of all keys below 2^-64: the result's factor in two steps, both normal
       const float split = am > 64.0f ? 64.0f : 0.0f;
       const float il = 1.0f / l * pow2i(split - am);
+      const bool in_two = __any_sync(0xffffffffu, split != 0.0f);  // one way for the warp
 #pragma unroll 1
       for (int ch = 0; ch < kHeadDim / 32; ++ch) {
         uint32_t ov[32];
@@ -976,7 +978,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(o[i]);
           }
         }
-        if (split != 0.0f) {
+        if (in_two) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             ov[i] = __float_as_uint(__uint_as_float(ov[i]) * pow2i(-split));

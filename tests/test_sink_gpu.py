@@ -111,6 +111,14 @@ def test_v_rows_of_mixed_magnitude():
     check_forward(x, 4)
 
 
+def test_tiny_v_rows_beside_ordinary_ones():
+    """The rows of one warp need different scales."""
+    x = su.draw(1, 300, 4, 2, seed=72)
+    x["v"][0, :100] = (x["v"][0, :100].float() * 1e-30).to(torch.bfloat16)
+    x["v"][0, 101:105] = (x["v"][0, 101:105].float() * 1e30).to(torch.bfloat16)
+    check_forward(x, 0)
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_values_that_are_not_finite_reach_only_rows_that_see_them(bad):
     """Rows behind a padded sequence, keys out of the window: a masked key has no part
