@@ -36,12 +36,15 @@
 // What bounds it: the regions' chain per unit (64 tokens of two heads), about 27,000
 // cycles of which the MMAs are 1,700: Q' 2.4k, K' 3.5k and V 2k of the owner, maximum
 // 2k, P 4.9k, gate and store 7.5k, waits for S and O 3.5k.  4 x 4096 tokens of 32 heads:
-// 223 us, 32 % of the measured copy rate (the plain forward: 143 us, without the
+// 232 - 238 us, 30 % of the measured copy rate (the plain forward: 143 us, without the
 // maximum, with 128-token tiles and bf16 operands).  Measured instead:
 //   - warp MMAs (m16n8k16) on 16 tokens x 2 heads per warp, S, P and O in registers,
 //     eight warps per SM: 320 us (their operands' shared-memory reads and latency);
 //     with 16 warps and one head each, bf16 P and spills: 252 us.
 //   - K' and V by a helper warp in the background: 336 us, one warp is too slow.
+//   - work moved from the region of a tile's first pair to the other, whose chain is
+//     shorter: V 246 us, the next tile's K' 258 us (against 232 in the same minutes).
+//     Side by side in one phase the regions get in each other's way.
 #include <atomic>
 
 #include "launch.cuh"
