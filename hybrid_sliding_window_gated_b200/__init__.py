@@ -115,13 +115,17 @@ def _ptr(t):
     return None if t is None else t.data_ptr()  # argtypes turn it into a void pointer
 
 
+def _current_device():
+    if not torch.cuda.is_initialized():
+        torch.cuda.init()
+    return torch._C._cuda_getDevice()
+
+
 def _stream(stream):
     if stream is not None:
         return stream.cuda_stream
-    if not torch.cuda.is_initialized():
-        torch.cuda.init()
     # the pointer alone: a torch.cuda.Stream object around it costs 3 us
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return torch._C._cuda_getCurrentRawStream(_current_device())
 
 
 def _check(rc, where):
@@ -136,14 +140,16 @@ def _need(where, device, **tensors):
     that many elements; the kernels take its pointer and the sizes in the
     parameter block, so anything else would be misread or overrun."""
     index = device.index
-    for t, dtype, n in tensors.values():  # one pass; a call in order ends here
-        if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
-            break
-        if n > 0 and not (t.is_cuda and t.get_device() == index and t.is_contiguous()
-                          and t.numel() >= n):
-            break
-    else:
-        return
+    try:
+        for t, dtype, n in tensors.values():  # one pass; a call in order ends here
+            if t.dtype is not dtype or n > 0 and (t.get_device() != index or t.numel() < n
+                                                  or not t.is_contiguous()):
+                break
+        else:
+            if device.type == "cuda":
+                return
+    except AttributeError:  # not a tensor: named below
+        pass
     for name, (t, dtype, n) in tensors.items():
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{where}: {name} must be a torch.Tensor")
@@ -164,9 +170,9 @@ def _need(where, device, **tensors):
 
 def _on_current_device(where, device):
     """The library launches on the current device, whatever device the tensors are on."""
-    if device.type == "cuda" and device.index != torch.cuda.current_device():
+    if device.type == "cuda" and device.index != _current_device():
         raise ValueError(f"{where}: the tensors are on {device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+                         f"cuda:{_current_device()}")
 
 
 def make_params(B, T, Hq, Hkv, *, head_dim=128, window=128, rot_dim=42, rope_base=1e4, eps=1e-6,

@@ -43,8 +43,8 @@
 //     with 16 warps and one head each, bf16 P and spills: 252 us.
 //   - K' and V by a helper warp in the background: 336 us, one warp is too slow.
 //   - work moved from the region of a tile's first pair to the other, whose chain is
-//     shorter: V 246 us, the next tile's K' 258 us (against 232 in the same minutes).
-//     Side by side in one phase the regions get in each other's way.
+//     shorter: V 246 us, the next tile's K' 258 us (against 232 in the same minutes;
+//     why was not found).
 #include <atomic>
 
 #include "launch.cuh"

@@ -188,7 +188,7 @@ def test_binding_refuses_wrong_tensors(L):
 
 
 def test_tensors_on_another_device_refused(monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(swa, "_current_device", lambda: 1)
     swa._on_current_device("f", torch.device("cuda", 1))
     with pytest.raises(ValueError, match="current device is cuda:1"):
         swa._on_current_device("f", torch.device("cuda", 0))
