@@ -36,15 +36,19 @@
 // What bounds it: the regions' chain per unit (64 tokens of two heads), about 27,000
 // cycles of which the MMAs are 1,700: Q' 2.4k, K' 3.5k and V 2k of the owner, maximum
 // 2k, P 4.9k, gate and store 7.5k, waits for S and O 3.5k.  4 x 4096 tokens of 32 heads:
-// 232 - 238 us, 30 % of the measured copy rate (the plain forward: 143 us, without the
-// maximum, with 128-token tiles and bf16 operands).  Measured instead:
+// 230 us, 31 % of the measured copy rate (the plain forward: 143 us, without the
+// maximum, with 128-token tiles and bf16 operands).  A run starts with its first K tiles
+// loaded straight into the ring and shared by the regions, and the tokens' rotations
+// evaluated once per CTA: 1 x 256 tokens of 4 / 1 heads 28.5 -> 26.3 us.  Measured instead:
 //   - warp MMAs (m16n8k16) on 16 tokens x 2 heads per warp, S, P and O in registers,
 //     eight warps per SM: 320 us (their operands' shared-memory reads and latency);
 //     with 16 warps and one head each, bf16 P and spills: 252 us.
 //   - K' and V by a helper warp in the background: 336 us, one warp is too slow.
 //   - work moved from the region of a tile's first pair to the other, whose chain is
 //     shorter: V 246 us, the next tile's K' 258 us (against 232 in the same minutes;
-//     why was not found).
+//     why was not found);
+//   - a run's first V tiles by the second region before its first S: 24.5 us at 1 x 256,
+//     but 240 us here, for the second copy of that code.
 #include <atomic>
 
 #include "launch.cuh"
@@ -77,7 +81,7 @@ struct alignas(1024) Smem {
   float va[kRing];                     // a of each V row (v 2^a is stored)
   int scaled[kSlots + 1];              // some row of the slot (or a sink) has a != 0
   float cc;                            // cq ck
-  uint64_t rotfull[4], stgfull, stgempty, kready[3], kempty[3];
+  uint64_t rotfull[4], runfull, stgfull, stgempty, kready[3], kempty[3];
   uint64_t vfull[3], vready[3], vempty[3];
   uint64_t skfull, skready, skempty, svfull, svready, svempty;  // the sinks' K and V
   uint64_t qfull[3], qready[2], sfull[2], pfull[2], ofull[2], tfree[2];
@@ -356,6 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) mbar_init(&sm.rotfull[i], 1);
+    mbar_init(&sm.runfull, 1);  // the run's first K tiles
     mbar_init(&sm.stgfull, 1);
     mbar_init(&sm.stgempty, 128);
     mbar_init(&sm.skfull, 1);
@@ -399,6 +404,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&sm.tmem_base, 512);
     tmem_relinquish();
   }
+  // rot(tok w_p) of the tile's 64 tokens, evaluated once for all threads, in a Q slot
+  // that no copy uses before the second barrier below
+  float2* tok_rot = reinterpret_cast<float2*>(sm.q[2]);
+  for (int i = tid; i < kPairs * kTok; i += kThreads) {
+    float cv, sv;
+    rope_cos_sin(static_cast<double>(i & (kTok - 1)), a.inv_freq[i / kTok], &cv, &sv);
+    tok_rot[i] = make_float2(cv, sv);
+  }
+  fence_proxy_async_smem();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   {
@@ -416,6 +430,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort = &sm.abort;
   const bool sinks = a.n_sink > 0;
+  const int pre = min(2, cursor_at(a, u0).t);  // tiles loaded before the run's first
+  RowRot<kPairs> rr;  // of a region thread's rows of Q, K and V, which are one token's
+  if (warp >= 4) {
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p) rr.r[p] = tok_rot[p * kTok + (((tid - 128) & 127) >> 1)];
+  }
+  __syncthreads();
 
   if (warp < 4) {
     regs_dec<kRegsControl>();
@@ -445,9 +466,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       ok = load_q(c, 0);  // the first rows do not wait for the run's K tiles
       for (int it = 0; it < n_tiles && ok; ++it, next_tile(c, a)) {
-        // The tables of this tile's loads first: Q rows need the last one before any
-        // K has left the staging tile.  Load n - 4 is done with its table: load n - 2
-        // has been transformed into a slot that Q K^T of tile n - 3 or later freed.
+        // Tile it's load follows that of tile it - 1 out of the staging tile (tile 0's do
+        // not use it).
+        if (it >= 2 && !(ok = wait0(&sm.stgempty, it & 1, kSiteStgEmpty))) break;
+        // The tables of this tile's loads.  Table n % 4 is free: the loads before n are
+        // done with theirs, and load n - 1 was transformed into a slot that Q K^T of load
+        // n - 4's tile or a later one freed, so that tile's Q rows are too.
         for (int j = first_load(c); j <= c.t; ++j) {
           const int n = nk + j - first_load(c);
           if (lane < kPairs) {
@@ -458,12 +482,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.rotfull[n & 3]);
         }
-        for (int j = first_load(c); j <= c.t && ok; ++j) {
-          if (nk > 0 && !(ok = wait0(&sm.stgempty, (nk - 1) & 1, kSiteStgEmpty))) break;
+        if (it == 0) {  // the run's first tiles at once, straight into the ring
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.runfull, (pre + 1) * 2 * kTileHalf);
+            for (int j = c.t - pre; j <= c.t; ++j) {
+              const int s = j % kSlots;
+              tma_load_4d(sm.k[0] + s * kTileHalf, &tm_k, &sm.runfull, 0, c.kvh, j * kTok, c.b);
+              tma_load_4d(sm.k[1] + s * kTileHalf, &tm_k, &sm.runfull, 64, c.kvh, j * kTok, c.b);
+            }
+          }
+          nk = pre + 1;
+        } else {
           if (lane == 0) {
             mbar_arrive_expect_tx(&sm.stgfull, 2 * kTileHalf);
-            tma_load_4d(sm.stage[0], &tm_k, &sm.stgfull, 0, c.kvh, j * kTok, c.b);
-            tma_load_4d(sm.stage[1], &tm_k, &sm.stgfull, 64, c.kvh, j * kTok, c.b);
+            tma_load_4d(sm.stage[0], &tm_k, &sm.stgfull, 0, c.kvh, c.t * kTok, c.b);
+            tma_load_4d(sm.stage[1], &tm_k, &sm.stgfull, 64, c.kvh, c.t * kTok, c.b);
           }
           ++nk;
         }
@@ -481,7 +514,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int h = it == 0 ? 1 : 0; h < pairs && ok; ++h) ok = load_q(c, h);
       }
       if (!ok && lane == 0) {  // copies in flight land before the CTA's memory is released
-        if (nk > 0) mbar_wait_drain(&sm.stgfull, (nk - 1) & 1);
+        if (nk > 0) mbar_wait_drain(&sm.runfull, 0);
+        if (nk > pre + 1) mbar_wait_drain(&sm.stgfull, (nk - pre) & 1);
         if (ns > 0) mbar_wait_drain(&sm.skfull, (ns - 1) & 1);
         for (int s = 0; s < 3; ++s) {
           const int n = (nq - s + 2) / 3;
@@ -619,16 +653,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = (warp - 4) >> 2, wq4 = warp & 3;
     const int row = wq4 * 32 + lane, tok = row >> 1, head = row & 1;
     const uint32_t t_row = tmem + (static_cast<uint32_t>(wq4 * 32) << 16) + r * 256;
-    RowRot<kPairs> rr;  // rot(tok w_p): this thread's rows of Q, K and V are token tok's
-#pragma unroll
-    for (int p = 0; p < kPairs; ++p) {
-      float cv, sv;
-      rope_cos_sin(static_cast<double>(tok), a.inv_freq[p], &cv, &sv);
-      rr.r[p] = make_float2(cv, sv);
-    }
     const float sc = a.scale_log2 * sm.cc;
     const bool elected = row == 0;
-    const int pre = min(2, cursor_at(a, u0).t);  // tiles loaded before the run's first
     bool ok = true;
     // Every wait's outcome is the same for the whole warp: the TMEM accesses and
     // shuffles behind it are warp-wide.
@@ -671,15 +697,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool mine = owner && kacct == c.u;
         for (int j = first_load(kc); j <= kc.t && ok; ++j, ++nk) {
           const int s = j % kSlots;
-          if (mine) {
-            if (nk > 0 && !W(&sm.kready[last_s], kr.parity(last_s) ^ 1u, kSiteKReady)) break;
-            if (!W(&sm.stgfull, nk & 1, kSiteStgFull)) break;
-            if (kr.was_used(s) && !W(&sm.kempty[s], kr.parity(s) ^ 1u, kSiteKEmpty)) break;
-            k_row_pair<kPairs>(sm.stage[0], sm.stage[1], tok, sm.k[0], sm.k[1], s * kTok + tok,
-                               head, sm.wk, sm.rot_tile[nk & 3], rr, a.eps);
+          // the run's first tiles in place, by both regions where both start with them
+          const bool first = kacct == 0;
+          if (first ? (pairs > 1 ? ((kc.t - j) & 1) == r : r == 0) : mine) {
+            if (first) {
+              if (!W(&sm.rotfull[nk & 3], 0, kSiteRot)) break;
+              if (!W(&sm.runfull, 0, kSiteStgFull)) break;
+            } else {
+              if (!W(&sm.kready[last_s], kr.parity(last_s) ^ 1u, kSiteKReady)) break;
+              if (!W(&sm.stgfull, (nk - pre - 1) & 1, kSiteStgFull)) break;
+              if (kr.was_used(s) && !W(&sm.kempty[s], kr.parity(s) ^ 1u, kSiteKEmpty)) break;
+            }
+            const int at = s * kTok + tok;
+            k_row_pair<kPairs>(first ? sm.k[0] : sm.stage[0], first ? sm.k[1] : sm.stage[1],
+                               first ? at : tok, sm.k[0], sm.k[1], at, head, sm.wk,
+                               sm.rot_tile[nk & 3], rr, a.eps);
             fence_proxy_async_smem();
             mbar_arrive(&sm.kready[s]);
-            mbar_arrive(&sm.stgempty);
+            if (!first) mbar_arrive(&sm.stgempty);
           }
           kr.advance(s);
           last_s = s;
