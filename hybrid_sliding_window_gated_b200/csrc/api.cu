@@ -739,10 +739,7 @@ int swa_sink_fwd(const swa_params_t* p, int32_t n_sink, const swa_bf16_t* q, con
   a.scale_log2 = score_scale(p) * 1.4426950408889634f;
   a.eps = p->eps;
   a.flags = p->flags;
-  a.q = q;
-  a.k = k;
   a.v = v;
-  a.g = g;
   a.wq = wq;
   a.wk = wk;
   a.o = o;

@@ -1069,9 +1069,6 @@ int launch_global_fwd(int rot_dim, const CUtensorMap& tq, const CUtensorMap& tk,
   }
 }
 
-}  // namespace swa
-
-namespace swa {
 namespace glb {
 
 template <bool kShared>

@@ -90,7 +90,8 @@ __global__ void __launch_bounds__(256) sink_bwd_kv_kernel(const SinkBwdArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long gw = static_cast<long long>(blockIdx.x) * 8 + warp;
   if (gw >= static_cast<long long>(a.B) * a.Tp) return;
-  const int b = static_cast<int>(gw / a.Tp), t = static_cast<int>(gw - static_cast<long long>(b) * a.Tp);
+  const int b = static_cast<int>(gw / a.Tp);
+  const int t = static_cast<int>(gw - static_cast<long long>(b) * a.Tp);
   const int P = a.half_rot;
   float2 rot = make_float2(1.0f, 0.0f);
   if (lane < P) rope_cos_sin(static_cast<double>(t), a.inv_freq[lane], &rot.x, &rot.y);
@@ -545,7 +546,8 @@ __global__ void __launch_bounds__(kQThreads, 2) sink_bwd_q_kernel(const SinkBwdA
     }
     // the next head's rows, and this one's raw q for the end, towards L2
     {
-      const long long nx = hrow * kRowBytes + (h + 1 < h1 ? static_cast<long long>(a.Tp) * kRowBytes : 0);
+      const long long nx =
+          (hrow + (h + 1 < h1 ? static_cast<long long>(a.Tp) : 0)) * kRowBytes;
       asm volatile("prefetch.global.L2 [%0];" ::"l"(a.qr + nx + 128 * lane));
       asm volatile("prefetch.global.L2 [%0];" ::"l"(a.dr + nx + 128 * lane));
       const int t = min(i0 + (lane >> 1), a.T - 1);
@@ -656,7 +658,8 @@ constexpr float kPUp = 14.0f;
 
 // One block of 16 queries against a warp's 16 keys: P^T and dS^T, added into dv
 // and dk.  q' and dA rows of the block start at qt and dt, its row records at
-// `row`; am2 and fj carry 2^-kPUp, and dv 2^kPUp.  hide(key row, query column) masks, where `masked` says that any is.
+// `row`; am2 and fj carry 2^-kPUp, and dv 2^kPUp.  hide(key row, query column) masks,
+// where `masked` says that any is.
 template <typename Hide, typename VFrag>
 __device__ __forceinline__ void key_block(float (&dk)[16][4], float (&dv)[16][4],
                                           const uint32_t (&kf)[8][4], VFrag vfrag, uint32_t qt,
@@ -1121,15 +1124,17 @@ int launch_sink_bwd(const SinkBwdArgs& a, cudaStream_t stream) {
   const long long tiles = static_cast<long long>(a.B) * a.Hkv * a.tiles;
   const long long chains = static_cast<long long>(a.B) * a.Hkv;
   const long long row_warps = tokens / 16 * a.Hq;
-  if (row_warps / 8 > 0x7fffffffLL || tokens / 8 > 0x7fffffffLL || tiles * a.head_parts > 0x7fffffffLL || chains * 16 > 0x7fffffffLL)
+  if (row_warps / 8 > 0x7fffffffLL || tokens / 8 > 0x7fffffffLL ||
+      tiles * a.head_parts > 0x7fffffffLL || chains * 16 > 0x7fffffffLL ||
+      chains * a.chunks > 0x7fffffffLL)
     return SWA_ERR_UNSUPPORTED;
   const auto grid = [](long long n) { return static_cast<unsigned>(n); };
   rc = launch_dependent(snk::sink_bwd_kv_kernel, grid((tokens + 7) / 8), 256, 0, stream, a);
   if (rc == SWA_OK)
     rc = launch_dependent(snk::sink_bwd_rows_kernel, grid((row_warps + 7) / 8), 256, 0, stream, a);
   if (rc == SWA_OK)
-    rc = launch_dependent(snk::sink_bwd_q_kernel, grid(tiles * a.head_parts), snk::kQThreads, sizeof(snk::QSmem),
-                          stream, a);
+    rc = launch_dependent(snk::sink_bwd_q_kernel, grid(tiles * a.head_parts), snk::kQThreads,
+                          sizeof(snk::QSmem), stream, a);
   if (rc == SWA_OK && a.n_sink > 0) {
     rc = launch_dependent(snk::sink_bwd_sink_kernel, grid(chains * a.chunks), 32 * snk::kSWarps,
                           sizeof(snk::SSmem), stream, a);

@@ -58,7 +58,8 @@ struct Control {
   uint64_t rows[kMaxStages], full[kMaxStages], empty[kMaxStages], never;
   int abort;
 };
-static_assert(kGroupWarps * kDecMaxGroup * kOStride * 4 <= 2 * kHalf, "partial O does not fit the K ring");
+static_assert(kGroupWarps * kDecMaxGroup * kOStride * 4 <= 2 * kHalf,
+              "partial O does not fit the K ring");
 
 // Behind Control, for each group: q' as bf16 pairs, [2 G][kQStride] words (the heads,
 // then their remainders).
@@ -127,8 +128,8 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
 // krow + kstep j is the K row of n-tile j that this lane fetches, vrow its V row.  Keys
 // that valid(key) refuses are masked; their V rows are finite.
 template <int NT, typename Valid>
-__device__ __forceinline__ void attend(uint32_t kbase, uint32_t vbase, int half, int krow, int kstep,
-                                       int vrow, const uint32_t* qh, const uint32_t* ql,
+__device__ __forceinline__ void attend(uint32_t kbase, uint32_t vbase, int half, int krow,
+                                       int kstep, int vrow, const uint32_t* qh, const uint32_t* ql,
                                        bool row_ok, float scale_log2, int lane, Valid&& valid,
                                        float& m, float& l, float (&oacc)[16][4]) {
   const int tig = lane & 3;
@@ -449,8 +450,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int s = i % a.stages;
       const long long u = u0 + i;
       const int n = static_cast<int>(u / a.Hkv), kvh = static_cast<int>(u - u / a.Hkv * a.Hkv);
-      if (!process_unit(Stage{base + s * a.stage_bytes, a.s8, a.G}, sm.grp[gi], qa, a, n, kvh, gi, lw,
-                        lane, &sm.rows[s], &sm.full[s], (i / a.stages) & 1, abort))
+      if (!process_unit(Stage{base + s * a.stage_bytes, a.s8, a.G}, sm.grp[gi], qa, a, n, kvh, gi,
+                        lw, lane, &sm.rows[s], &sm.full[s], (i / a.stages) & 1, abort))
         break;
       group_and(true, 1 + gi);
       if (lw == 0 && lane == 0) mbar_arrive(&sm.empty[s]);
@@ -505,7 +506,8 @@ int launch_sink_decode(const CUtensorMap& tk, const CUtensorMap& tv, const CUten
   int rc = current_device_info(&di);
   if (rc != SWA_OK) return rc;
   constexpr int kLimit = 232448;
-  const int fixed = static_cast<int>(sizeof(snd::Control)) + snd::kGroups * snd::qa_bytes(a.G) + 1024;
+  const int fixed =
+      static_cast<int>(sizeof(snd::Control)) + snd::kGroups * snd::qa_bytes(a.G) + 1024;
   a.stage_bytes = snd::stage_size(a.s8, a.G);
   // Three units in flight where they fit (up to 8 sinks, or 16 with few heads), else two.
   a.stages = 3 * a.stage_bytes + fixed <= kLimit ? 3 : 2;

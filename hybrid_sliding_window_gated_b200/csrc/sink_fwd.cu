@@ -127,7 +127,9 @@ __device__ __forceinline__ void next_pair(Cursor& c, const SinkFwdArgs& a) {
   }
 }
 // First tile to load at this tile: the two before it at the start of a run.
-__device__ __forceinline__ int first_load(const Cursor& c) { return c.u == 0 ? max(0, c.t - 2) : c.t; }
+__device__ __forceinline__ int first_load(const Cursor& c) {
+  return c.u == 0 ? max(0, c.t - 2) : c.t;
+}
 __device__ __forceinline__ bool seg_first(const Cursor& c) { return c.u == 0 || c.t == 0; }
 __device__ __forceinline__ bool seg_last(const Cursor& c, const SinkFwdArgs& a, int n_tiles) {
   return c.u == n_tiles - 1 || c.t == a.tiles - 1;

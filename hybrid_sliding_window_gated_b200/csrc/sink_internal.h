@@ -18,13 +18,10 @@ struct SinkFwdArgs {
   float scale_log2;          // softmax scale * log2(e)
   float eps;
   int flags;
-  const uint16_t* q;
-  const uint16_t* k;
-  const uint16_t* v;
-  const uint16_t* g;
+  const uint16_t* v;         // [B, T, Hkv, D], for rows that are summed key by key
   const float* wq;
   const float* wk;
-  uint16_t* o;
+  uint16_t* o;               // [B, T, Hq, D]
   float* lse;                // [B, Hq, T] or null
   int* err;
   double inv_freq[kMaxPairs];

@@ -82,3 +82,12 @@ def args(x, dev=None, dtype=None):
 def rel(got, ref):
     got, ref = got.detach().double().cpu(), ref.detach().double().cpu()
     return float((got - ref).norm() / ref.norm().clamp_min(1e-300))
+
+
+def neighbours(got, want):
+    """Where a bf16 cache holds the same bits as the 64-bit form's, or an entry that fp32
+    arithmetic may round otherwise: k' = u c - v s of |u|, |v| <= 12 max|w| < 16.9 with six
+    fp32 roundings, 6 x 2^-24 x 2 x 16.9 < 2^-16, and then the neighbouring bf16 value."""
+    a, b = got.double(), want.double()
+    return (got.view(torch.int16) == want.view(torch.int16)) | (
+        (a - b).abs() <= 2.0 ** -7 * b.abs() + 2.0 ** -16)

@@ -298,10 +298,10 @@ def test_decode(Hq, Hkv, S, R):
     ok()
     ref = decode_ref(pos, *x, *caches, R, 1e4)
     assert torch.isfinite(o).all() and su.rel(o, ref) <= REL
-    for got, want in zip(dev, caches):  # k' may round to the neighbouring bf16 value
-        got = got.cpu().view(torch.int16).int()
-        want = want.view(torch.int16).int()
-        assert ((got - want).abs() <= 1).all() and (got != want).sum() <= 1e-3 * got.numel()
+    for got, want in zip(dev, caches):
+        got = got.cpu()
+        same = got.view(torch.int16) == want.view(torch.int16)
+        assert su.neighbours(got, want).all() and (~same).sum() <= 1e-3 * same.numel()
 
 
 def test_decode_bad_position_is_skipped_and_reported():
