@@ -121,8 +121,8 @@ __device__ __forceinline__ void rest_pos(int lane, int* chunk0, int* byte) {
 }
 
 // k' / ck of N rows, fp16, in rope order into rows r0 .. of `tile`; w_* are this lane's
-// weights divided by ck, rot its pair's
-// rotation at each row's position.  The rows' chains of shuffles run side by side.
+// weights divided by ck, rot its pair's rotation at each row's position.  The rows' chains
+// of shuffles run side by side.
 template <int N>
 __device__ __forceinline__ void store_k_rows(uint8_t* tile, int r0, const KRow (&x)[N], int lane,
                                              float w_lo, float w_hi, float4 w_rest,
