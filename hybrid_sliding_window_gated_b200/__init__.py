@@ -6,10 +6,13 @@ the library's sm_100a kernels.  If the compiled library is missing, importing
 the binding raises, so there is no silent CPU fallback.
 
 PyTorch serves as the owner of device memory and streams: tensors are passed
-by ``data_ptr()`` and calls are enqueued on the current CUDA stream.  Before a
-pointer is passed, each tensor's dtype, element count, contiguity and device
-are checked against what the call reads or writes (``TypeError`` /
-``ValueError``); the library itself checks the sizes and alignment.
+by ``data_ptr()`` and calls are enqueued on the current CUDA stream, or on the one
+given as ``stream``: what a call makes itself (outputs, scratch) is then made on that
+stream, and the caller orders the inputs before the call, keeps them until it is done,
+and orders the use of its results behind it.  Before a pointer is passed, each
+tensor's dtype, element count, contiguity and device are checked against what the call
+reads or writes (``TypeError`` / ``ValueError``); the library itself checks the sizes
+and alignment.
 """
 import ctypes
 import os
@@ -128,6 +131,34 @@ def _stream(stream):
     return torch._C._cuda_getCurrentRawStream(_current_device())
 
 
+def _new(stream, make, *args, device, shared=True, **kw):
+    """A tensor that the call makes itself.  With a ``stream`` argument it is allocated and
+    filled on that stream, in order with the call's kernels; where the caller receives it
+    (``shared``), its memory goes to no other allocation while work of the current stream,
+    where the caller goes on, still uses it."""
+    if stream is None or device.type != "cuda":
+        return make(*args, device=device, **kw)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = make(*args, device=device, **kw)
+    if shared:
+        t.record_stream(here)
+    return t
+
+
+def _grads(stream, q, k, v, g):
+    """What a backward writes (dq, dk, dv, dg) and adds into (dwq, dwk, from zero)."""
+    D, device = q.shape[-1], q.device
+    return (*(_new(stream, torch.empty_like, t, device=device) for t in (q, k, v, g)),
+            *(_new(stream, torch.zeros, D, dtype=torch.float32, device=device) for _ in range(2)))
+
+
+def _scratch(stream, device, nbytes):
+    return _new(stream, torch.empty, max(nbytes, 1), dtype=torch.uint8, device=device, shared=False)
+
+
 def _check(rc, where):
     if rc != OK:
         raise SwaError(rc, where)
@@ -190,9 +221,9 @@ def fwd(q, k, v, g, wq, wk, *, window=128, rot_dim=42, rope_base=1e4, eps=1e-6, 
     B, T, Hq, D = q.shape
     Hkv = k.shape[2]
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, torch.empty_like, q, device=q.device)
     if want_lse and lse is None:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
+        lse = _new(stream, torch.empty, (B, Hq, T), dtype=torch.float32, device=q.device)
     p = make_params(B, T, Hq, Hkv, head_dim=D, window=window, rot_dim=rot_dim,
                     rope_base=rope_base, eps=eps, scale=scale, flags=flags)
     nq, nk = B * T * Hq * D, B * T * Hkv * D
@@ -213,9 +244,9 @@ def fwd_halo(q, k, v, g, wq, wk, k_halo, v_halo, pos0, *, window=128, rot_dim=42
     B, T, Hq, D = q.shape
     Hkv = k.shape[2]
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, torch.empty_like, q, device=q.device)
     if want_lse and lse is None:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
+        lse = _new(stream, torch.empty, (B, Hq, T), dtype=torch.float32, device=q.device)
     p = make_params(B, T, Hq, Hkv, head_dim=D, window=window, rot_dim=rot_dim,
                     rope_base=rope_base, eps=eps, scale=scale, flags=flags)
     nq, nk, nh = B * T * Hq * D, B * T * Hkv * D, B * (window - 1) * Hkv * D
@@ -242,9 +273,9 @@ def fwd_fp8(q8, k8, v8, qkv_scale, g, wq, wk, *, window=128, rot_dim=42, rope_ba
     B, T, Hq, D = q8.shape
     Hkv = k8.shape[2]
     if out is None:
-        out = torch.empty(q8.shape, dtype=torch.bfloat16, device=q8.device)
+        out = _new(stream, torch.empty, q8.shape, dtype=torch.bfloat16, device=q8.device)
     if want_lse and lse is None:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q8.device)
+        lse = _new(stream, torch.empty, (B, Hq, T), dtype=torch.float32, device=q8.device)
     byte = lambda t: t.view(torch.uint8) if t.dtype == torch.float8_e4m3fn else t
     q8, k8, v8 = byte(q8), byte(k8), byte(v8)
     p = make_params(B, T, Hq, Hkv, head_dim=D, window=window, rot_dim=rot_dim,
@@ -287,13 +318,11 @@ def bwd(q, k, v, g, wq, wk, lse, dO, *, window=128, rot_dim=42, rope_base=1e4, e
     p = make_params(B, T, Hq, Hkv, head_dim=D, window=window, rot_dim=rot_dim,
                     rope_base=rope_base, eps=eps, scale=scale, flags=flags)
     if grads is None:
-        grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(g),
-                 torch.zeros(D, dtype=torch.float32, device=q.device),
-                 torch.zeros(D, dtype=torch.float32, device=q.device))
+        grads = _grads(stream, q, k, v, g)
     dq, dk, dv, dg, dwq, dwk = grads
     nbytes = int(lib().swa_bwd_workspace_size(ctypes.byref(p)))
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(stream, q.device, nbytes)
     _need_bwd("swa_bwd", q, k, v, g, wq, wk, lse, dO, grads,
               workspace=(workspace, torch.uint8, nbytes))
     rc = lib().swa_bwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(wq), _ptr(wk),
@@ -314,15 +343,14 @@ def bwd_edges(q, k, v, g, wq, wk, lse, dO, n_lo, n_hi, *, window=128, rot_dim=42
     p = make_params(B, T, Hq, Hkv, head_dim=D, window=window, rot_dim=rot_dim,
                     rope_base=rope_base, eps=eps, scale=scale)
     if grads is None:
-        grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(g),
-                 torch.zeros(D, dtype=torch.float32, device=q.device),
-                 torch.zeros(D, dtype=torch.float32, device=q.device))
+        grads = _grads(stream, q, k, v, g)
     dq, dk, dv, dg, dwq, dwk = grads
     nbytes = int(lib().swa_bwd_workspace_size(ctypes.byref(p)))
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
-    lo = torch.empty((B, n_lo, Hkv, 2, D), dtype=torch.float32, device=q.device) if n_lo else None
-    hi = torch.empty((B, n_hi, Hkv, 2, D), dtype=torch.float32, device=q.device) if n_hi else None
+        workspace = _scratch(stream, q.device, nbytes)
+    edge = lambda n: _new(stream, torch.empty, (B, n, Hkv, 2, D), dtype=torch.float32,
+                          device=q.device)
+    lo, hi = edge(n_lo) if n_lo else None, edge(n_hi) if n_hi else None
     extra = {"workspace": (workspace, torch.uint8, nbytes)}
     if lo is not None:
         extra["dkv_lo"] = (lo, torch.float32, lo.numel())
@@ -348,15 +376,14 @@ def bwd_halo(q, k, v, g, wq, wk, lse, dO, k_halo, v_halo, pos0, n_hi=0, *, windo
     p = make_params(B, T, Hq, Hkv, head_dim=D, window=window, rot_dim=rot_dim,
                     rope_base=rope_base, eps=eps, scale=scale)
     if grads is None:
-        grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(g),
-                 torch.zeros(D, dtype=torch.float32, device=q.device),
-                 torch.zeros(D, dtype=torch.float32, device=q.device))
+        grads = _grads(stream, q, k, v, g)
     dq, dk, dv, dg, dwq, dwk = grads
     nbytes = int(lib().swa_bwd_workspace_size(ctypes.byref(p)))
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
-    halo = torch.empty((B, window - 1, Hkv, 2, D), dtype=torch.float32, device=q.device)
-    hi = torch.empty((B, n_hi, Hkv, 2, D), dtype=torch.float32, device=q.device) if n_hi else None
+        workspace = _scratch(stream, q.device, nbytes)
+    edge = lambda n: _new(stream, torch.empty, (B, n, Hkv, 2, D), dtype=torch.float32,
+                          device=q.device)
+    halo, hi = edge(window - 1), edge(n_hi) if n_hi else None
     nh = B * (window - 1) * Hkv * D
     extra = {"workspace": (workspace, torch.uint8, nbytes),
              "k_halo": (k_halo, torch.bfloat16, nh), "v_halo": (v_halo, torch.bfloat16, nh)}
@@ -380,9 +407,7 @@ def bwd_noalloc(q, k, v, g, wq, wk, lse, dO, *, window=128, rot_dim=42, rope_bas
     p = make_params(B, T, Hq, Hkv, head_dim=D, window=window, rot_dim=rot_dim,
                     rope_base=rope_base, eps=eps, scale=scale)
     if grads is None:
-        grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(g),
-                 torch.zeros(D, dtype=torch.float32, device=q.device),
-                 torch.zeros(D, dtype=torch.float32, device=q.device))
+        grads = _grads(stream, q, k, v, g)
     dq, dk, dv, dg, dwq, dwk = grads
     _need_bwd("swa_bwd_noalloc", q, k, v, g, wq, wk, lse, dO, grads)
     rc = lib().swa_bwd_noalloc(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(wq),
@@ -398,7 +423,7 @@ def decode_step(pos, q, k_new, v_new, g, wq, wk, k_cache, v_cache, *, rot_dim=42
     N, Hq, D = q.shape
     Hkv, W = k_cache.shape[1], k_cache.shape[2]
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, torch.empty_like, q, device=q.device)
     p = make_params(N, 1, Hq, Hkv, head_dim=D, window=W, rot_dim=rot_dim, rope_base=rope_base,
                     eps=eps, scale=scale, flags=flags)
     nq, nk = N * Hq * D, N * Hkv * D
@@ -443,9 +468,9 @@ def global_fwd(q, k, v, wq, wk, k_cache, v_cache, *, rot_dim=42, rope_base=1e4, 
     Hkv = k.shape[2]
     cap = k_cache.shape[2]
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, torch.empty_like, q, device=q.device)
     if want_lse and lse is None:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
+        lse = _new(stream, torch.empty, (B, Hq, T), dtype=torch.float32, device=q.device)
     p = make_params(B, T, Hq, Hkv, head_dim=D, window=0, rot_dim=rot_dim, rope_base=rope_base,
                     eps=eps, scale=scale, flags=flags)
     nq, nk = B * T * Hq * D, B * T * Hkv * D
@@ -475,12 +500,12 @@ def global_decode_step(pos, q, k_new, v_new, wq, wk, k_cache, v_cache, *, rot_di
     N, Hq, D = q.shape
     Hkv, cap = k_cache.shape[1], k_cache.shape[2]
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, torch.empty_like, q, device=q.device)
     p = make_params(N, 1, Hq, Hkv, head_dim=D, window=0, rot_dim=rot_dim, rope_base=rope_base,
                     eps=eps, scale=scale, flags=flags)
     nbytes = int(lib().swa_global_decode_workspace_size(ctypes.byref(p), cap))
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(stream, q.device, nbytes)
     nq, nk = N * Hq * D, N * Hkv * D
     bf, f32 = torch.bfloat16, torch.float32
     _need("swa_global_decode_step", q.device, pos=(pos, torch.int64, N), q=(q, bf, nq),
@@ -527,9 +552,9 @@ def sink_fwd(q, k, v, g, wq, wk, n_sink, *, window=128, rot_dim=42, rope_base=1e
     B, T, Hq, D = q.shape
     Hkv = k.shape[2]
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, torch.empty_like, q, device=q.device)
     if want_lse and lse is None:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
+        lse = _new(stream, torch.empty, (B, Hq, T), dtype=torch.float32, device=q.device)
     p = make_params(B, T, Hq, Hkv, head_dim=D, window=window, rot_dim=rot_dim,
                     rope_base=rope_base, eps=eps, scale=scale, flags=flags)
     nq, nk = B * T * Hq * D, B * T * Hkv * D
@@ -558,13 +583,11 @@ def sink_bwd(q, k, v, g, wq, wk, o, lse, dO, n_sink, *, window=128, rot_dim=42, 
     p = make_params(B, T, Hq, Hkv, head_dim=D, window=window, rot_dim=rot_dim,
                     rope_base=rope_base, eps=eps, scale=scale, flags=flags)
     if grads is None:
-        grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(g),
-                 torch.zeros(D, dtype=torch.float32, device=q.device),
-                 torch.zeros(D, dtype=torch.float32, device=q.device))
+        grads = _grads(stream, q, k, v, g)
     dq, dk, dv, dg, dwq, dwk = grads
     nbytes = int(lib().swa_sink_bwd_workspace_size(ctypes.byref(p), n_sink))
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(stream, q.device, nbytes)
     _on_current_device("swa_sink_bwd", q.device)
     _need_bwd("swa_sink_bwd", q, k, v, g, wq, wk, lse, dO, grads,
               o=(o, torch.bfloat16, B * T * Hq * D), workspace=(workspace, torch.uint8, nbytes))
@@ -585,7 +608,7 @@ def sink_decode_step(pos, q, k_new, v_new, g, wq, wk, k_cache, v_cache, k_sink, 
     N, Hq, D = q.shape
     Hkv, W, S = k_cache.shape[1], k_cache.shape[2], k_sink.shape[2]
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, torch.empty_like, q, device=q.device)
     p = make_params(N, 1, Hq, Hkv, head_dim=D, window=W, rot_dim=rot_dim, rope_base=rope_base,
                     eps=eps, scale=scale, flags=flags)
     nq, nk = N * Hq * D, N * Hkv * D
@@ -646,12 +669,12 @@ def global_decode_shared(pos, q, k_new, v_new, wq, wk, k_prefix, v_prefix, prefi
         raise ValueError("swa_global_decode_shared: k_prefix holds more than one sequence")
     pcap = k_prefix.shape[-2]
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, torch.empty_like, q, device=q.device)
     p = make_params(N, 1, Hq, Hkv, head_dim=D, window=0, rot_dim=rot_dim, rope_base=rope_base,
                     eps=eps, scale=scale, flags=flags)
     nbytes = int(lib().swa_global_decode_shared_workspace_size(ctypes.byref(p), prefix_len, cap))
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(stream, q.device, nbytes)
     nq, nk = N * Hq * D, N * Hkv * D
     npre = Hkv * pcap * D if N and prefix_len else 0
     bf, f32 = torch.bfloat16, torch.float32
