@@ -121,12 +121,13 @@ __global__ void __launch_bounds__(256) sink_bwd_kv_kernel(const SinkBwdArgs a) {
     }
     v_absmax<kN>(v, m);
     const float2 rot1[1] = {rot};
+    const float eps1[1] = {real ? a.eps : 1.0f};
 #pragma unroll
     for (int e = 0; e < kN; ++e) {
       // a row's chunks lie as row t & 7 of a tile
       uint8_t* kt = stage[warp][0] + (e - (t & 7)) * kRowBytes;
       uint8_t* vt = stage[warp][1] + (e - (t & 7)) * kRowBytes;
-      store_k_rows<1>(kt, t & 7, x[e], lane, w_lo, w_hi, w_rest, rot1, a.eps);
+      store_k_rows<1>(kt, t & 7, x[e], lane, w_lo, w_hi, w_rest, rot1, eps1);
       const float ex = scale_exp(m[e]);
       store_v_row(vt, t & 7, v[e], lane, pow2i(ex));
       if (lane == 0 && h0 + e < a.Hkv)
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(256, 4) sink_bwd_rows_kernel(const SinkBwdArgs
     }
     __syncwarp();  // the rows have landed, and the stage has been read out
     float2 u0[kN], u1[kN];
-    float m[kN];
+    float m[kN], eps[kN];
     KRow x[kN];
 #pragma unroll
     for (int e = 0; e < kN; ++e) {
@@ -239,6 +240,7 @@ __global__ void __launch_bounds__(256, 4) sink_bwd_rows_kernel(const SinkBwdArgs
       u1[e] = __fmul2_rn(d1, s1);
       const float2 y0 = __fmul2_rn(__fmul2_rn(d0, q0), n0), y1 = __fmul2_rn(__fmul2_rn(d1, q1), n1);
       const int t = t0 + i + e;
+      eps[e] = t < a.T ? a.eps : 1.0f;
       if (t < a.T)
         *reinterpret_cast<uint2*>(
             a.dg + ((static_cast<long long>(b) * a.T + t) * a.Hq + hq) * kHeadDim + 4 * lane) =
@@ -251,7 +253,7 @@ __global__ void __launch_bounds__(256, 4) sink_bwd_rows_kernel(const SinkBwdArgs
     // the stage holds rows i & 7 .. of an eight-row tile
     uint8_t* qt = stage[warp][0] - (i & 7) * kRowBytes;
     uint8_t* dt = stage[warp][1] - (i & 7) * kRowBytes;
-    store_k_rows<kN>(qt, i & 7, x, lane, w_lo, w_hi, w_rest, rot, a.eps);
+    store_k_rows<kN>(qt, i & 7, x, lane, w_lo, w_hi, w_rest, rot, eps);
     const int md = lane >> 3, c = (lane & 7) >> 1, q = 2 * (lane & 1);
 #pragma unroll
     for (int e = 0; e < kN; ++e) {
@@ -344,7 +346,7 @@ __device__ __forceinline__ void norm_rope_back(const float (&acc)[16][4], const 
       x.rest[2 * i] = bf16_lo(rest[rr][i]);
       x.rest[2 * i + 1] = bf16_hi(rest[rr][i]);
     }
-    const float rinv = raw_rinv(x, eps);
+    const float rinv = raw_rinv(x, row < rows ? eps : 1.0f);  // zeros past them: not 0 inf
     float dot = 0.f;
     float yl[6], yh[6], yr[20];
 #pragma unroll

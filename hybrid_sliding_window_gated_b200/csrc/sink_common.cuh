@@ -121,12 +121,13 @@ __device__ __forceinline__ void rest_pos(int lane, int* chunk0, int* byte) {
 }
 
 // k' / ck of N rows, fp16, in rope order into rows r0 .. of `tile`; w_* are this lane's
-// weights divided by ck, rot its pair's rotation at each row's position.  The rows' chains
-// of shuffles run side by side.
+// weights divided by ck, rot its pair's rotation at each row's position.  eps of a row that
+// only fills up a tile is not 0, so that the row's zeros stay zeros.  The rows' chains of
+// shuffles run side by side.
 template <int N>
 __device__ __forceinline__ void store_k_rows(uint8_t* tile, int r0, const KRow (&x)[N], int lane,
                                              float w_lo, float w_hi, float4 w_rest,
-                                             const float2 (&rot)[N], float eps) {
+                                             const float2 (&rot)[N], const float (&eps)[N]) {
   float ss[N];
 #pragma unroll
   for (int e = 0; e < N; ++e) {
@@ -142,7 +143,7 @@ __device__ __forceinline__ void store_k_rows(uint8_t* tile, int r0, const KRow (
   uint32_t pair[N], r01[N], r23[N];
 #pragma unroll
   for (int e = 0; e < N; ++e) {
-    const float rinv = rsqrtf(ss[e] * (1.0f / kHeadDim) + eps);
+    const float rinv = rsqrtf(ss[e] * (1.0f / kHeadDim) + eps[e]);
     const float u = bf16_f32(x[e].lo) * rinv * w_lo, v = bf16_f32(x[e].hi) * rinv * w_hi;
     pair[e] = pack_f16x2(u * rot[e].x - v * rot[e].y, v * rot[e].x + u * rot[e].y);
     r01[e] = pack_f16x2(bf16_lo(x[e].rest.x) * rinv * w_rest.x,

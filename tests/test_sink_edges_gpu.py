@@ -144,3 +144,51 @@ def test_outputs_outlive_their_use_on_the_current_stream(name):
     torch.cuda.synchronize()
     same(name, kept, want)
     del junk
+
+
+# ------------------------------------------------------------------ eps = 0
+
+
+def cancelled(x, S):
+    """What fp16 dP costs dq, as a bound on its 2-norm over all rows (64 bits).  dS = P (dP - D)
+    cancels where a row's probability sits on few keys, as in a sequence's first tokens: dP
+    is off by 2^-11 of itself, so dq' by scale 2^-11 sum_j P |dP| |k'|, and RoPE and the norm
+    pass on at most max|w| / rms of that."""
+    q, k, v, g, wq, wk = su.args(x, dtype=torch.float64)
+    B, T, Hq, _ = q.shape
+    Hkv = k.shape[2]
+    G = Hq // Hkv
+    pos = torch.arange(T).expand(B, T)
+    qq, kk = su.norm_rope(q, wq, pos, 42, 1e4), su.norm_rope(k, wk, pos, 42, 1e4)
+    dA = x["dO"].double() * torch.sigmoid(g)
+    total = 0.0
+    for i in range(T):
+        js = su.visible(i, S, T)
+        heads = lambda y: y[:, i].reshape(B, Hkv, G, 128)
+        p = torch.softmax(torch.einsum("bhgd,bjhd->bhgj", heads(qq), kk[:, js]) / math.sqrt(128), -1)
+        dp = torch.einsum("bhgd,bjhd->bhgj", heads(dA), v[:, js])
+        size = kk[:, js].norm(dim=-1).permute(0, 2, 1)[:, :, None]
+        e = 2.0 ** -11 / math.sqrt(128) * (p * dp.abs() * size).sum(-1)
+        rms = heads(q).pow(2).mean(-1).sqrt()
+        total += float((e * wq.abs().max() / rms).pow(2).sum())
+    return math.sqrt(total)
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,S", [(1, 2, 2, 1, 4), (2, 65, 4, 2, 3), (1, 200, 3, 1, 16),
+                                          (1, 64, 2, 2, 0)])
+def test_backward_without_eps(B, T, Hq, Hkv, S):
+    """Tokens that only fill up the last tile have no norm: they take no part.  The 64-bit
+    form's eps of 1e-6 is a factor of 1 - 5e-7 on rows of mean square 1."""
+    x = su.draw(B, T, Hq, Hkv, seed=110 + T, grad=True)
+    t = su.args(x, DEV)
+    o, lse = swa.sink_fwd(*t, S, want_lse=True, eps=0.0)
+    grads = swa.sink_bwd(*t, o, lse, x["dO"].to(DEV), S, eps=0.0)
+    ok()
+    for name, got, want in zip(su.NAMES, grads, su.sink_gradients(su.args(x), x["dO"], S, 42, 1e4)):
+        assert torch.isfinite(got).all(), name
+        bound = REL_DG if name == "g" else REL
+        if name == "q":
+            bound += cancelled(x, S) / float(want.norm())
+        if name == "wq":  # sums of u RoPE^-1(dq') with |u| <= 4 and rows' errors of either sign
+            bound += 4 * cancelled(x, S) / float(want.norm())
+        assert su.rel(got, want) <= bound, name
