@@ -44,10 +44,10 @@
 // Numbers.  All products have fp16 operands and fp32 sums.  q' and k' are divided
 // by a power of two not below the norm weights (at most sqrt(128) then); a row
 // of dA is scaled by 2^b and one of v by 2^a so that its largest entry lies in
-// [1, 2): gradients and values of any magnitude keep fp16's 2^-12 rounding.  The
+// [1, 4): gradients and values of any magnitude keep fp16's 2^-12 rounding.  The
 // scales leave a product where its row or column index carries them; where an
 // index is summed over, the least exponent of the rows at hand takes their place,
-// and only entries far below the largest lose bits.  |dS| 2^(a + b) <= 1024.
+// and only entries far below the largest lose bits.  |dS| 2^(a + b) <= 2 x 128 x 2 x 4.
 #include <atomic>
 
 #include "launch.cuh"
@@ -58,17 +58,36 @@ namespace snk {
 
 constexpr float kNoScale = 126.0f;  // exponent of an all-zero row: takes part in no minimum
 
-// Exponent that brings m into [1, 2), or below 2^15 where that would take a factor
-// that is no normal fp32 number.
+// Exponent that brings m into [1, 2), or [2, 4) from 2^127 on, so that the factor is a
+// normal fp32 number; below 2 from 2^-126 down.
 __device__ __forceinline__ float scale_exp(float m) {
   if (!(m > 0.0f)) return kNoScale;
   const int e = static_cast<int>((__float_as_uint(m) >> 23) & 255u) - 127;
-  return static_cast<float>(max(-113, min(126, -e)));
+  return static_cast<float>(max(-126, min(126, -e)));
 }
-// v 2^x for whole x in [-252, 254], in two steps
+// v 2^x for whole x in [-252, 252], in two steps
 __device__ __forceinline__ float scale2(float v, float x) {
   const float h = truncf(0.5f * x);
   return v * pow2i(h) * pow2i(x - h);
+}
+
+// Factors f that make acc into acc v 2^x, for rows r and r + 8 of a fragment.  Beyond 2^100
+// (values and gradients both near the end of their range, though the sums need not be
+// large) a part of it is taken here, since the factor would leave fp32.
+__device__ __forceinline__ void split_scale(float (&acc)[16][4], float v, const float (&x)[2],
+                                            float (&f)[2]) {
+#pragma unroll
+  for (int rr = 0; rr < 2; ++rr) {
+    const float at = x[rr], over = fmaxf(at - 100.0f, 0.0f);
+    if (__any_sync(0xffffffffu, over > 0.0f)) {
+#pragma unroll
+      for (int n = 0; n < 16; ++n) {
+        acc[n][2 * rr] = scale2(acc[n][2 * rr], over);
+        acc[n][2 * rr + 1] = scale2(acc[n][2 * rr + 1], over);
+      }
+    }
+    f[rr] = scale2(v, at - over);
+  }
 }
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
@@ -264,7 +283,7 @@ __global__ void __launch_bounds__(256, 4) sink_bwd_rows_kernel(const SinkBwdArgs
           pack_f16x2(u0[e].x * f, u0[e].y * f);
       *reinterpret_cast<uint32_t*>(dt + row_off(r, 4 * md + q + 1) + 4 * c) =
           pack_f16x2(u1[e].x * f, u1[e].y * f);
-      if (lane == 0) a.row[out + i + e] = make_float4(l2[e], 0.f, be, 0.f);
+      if (lane == 0) a.row[out + i + e] = make_float4(l2[e], be, 0.f, 0.f);
     }
     if (i + kN < 16) fetch_row(i + kN);
     __syncwarp();
@@ -544,7 +563,7 @@ __global__ void __launch_bounds__(kQThreads, 2) sink_bwd_q_kernel(const SinkBwdA
               __ldg(reinterpret_cast<const uint32_t*>(drow + row_off(r + 8 * rr, 2 * kk + hf)));
         }
       L2[rr] = rec.x;
-      fs[rr] = scale2(a.scale * ck, -(rec.z + am));
+      fs[rr] = -(rec.y + am);
     }
     // the next head's rows, and this one's raw q for the end, towards L2
     {
@@ -618,7 +637,7 @@ __global__ void __launch_bounds__(kQThreads, 2) sink_bwd_q_kernel(const SinkBwdA
       Dn[rr] += __shfl_xor_sync(0xffffffffu, Dn[rr], 1);
       Dn[rr] += __shfl_xor_sync(0xffffffffu, Dn[rr], 2);
       if (c == 0)
-        reinterpret_cast<float*>(a.row + hrow + r + 8 * rr)[1] = Dn[rr] * pow2i(-am);
+        reinterpret_cast<float2*>(a.row + hrow + r + 8 * rr)[1] = make_float2(Dn[rr], am);
     }
     // ---- dQ = dS K', dS = P (dP - D)
     float dq[16][4];
@@ -644,6 +663,7 @@ __global__ void __launch_bounds__(kQThreads, 2) sink_bwd_q_kernel(const SinkBwdA
         mma_f16(dq[nd + 1], ds, kf[(nd >> 1) & 1][2], kf[(nd >> 1) & 1][3]);
       }
     }
+    split_scale(dq, a.scale * ck, fs, fs);
     norm_rope_back(dq, fs, sm.rope[w], a.q + raw, a.dq + raw, stride, rows,
                    a.rot + static_cast<long long>(i0) * kMaxPairs, a.wq, sm.dw[w], lane, P, a.eps);
   }
@@ -660,13 +680,13 @@ constexpr float kPUp = 14.0f;
 
 // One block of 16 queries against a warp's 16 keys: P^T and dS^T, added into dv
 // and dk.  q' and dA rows of the block start at qt and dt, its row records at
-// `row`; am2 and fj carry 2^-kPUp, and dv 2^kPUp.  hide(key row, query column) masks,
+// `row`; fj and D carry 2^-kPUp, and dv 2^kPUp.  hide(key row, query column) masks,
 // where `masked` says that any is.
 template <typename Hide, typename VFrag>
 __device__ __forceinline__ void key_block(float (&dk)[16][4], float (&dv)[16][4],
                                           const uint32_t (&kf)[8][4], VFrag vfrag, uint32_t qt,
                                           uint32_t dt, const float4* row, float sc, float bm,
-                                          float am2, const float (&fj)[2], uint32_t k_lane,
+                                          float am, const float (&fj)[2], uint32_t k_lane,
                                           uint32_t t_lane, int lane, bool masked, Hide hide) {
   const int r = lane >> 2, c = lane & 3;
   float s[2][4], dp[2][4];
@@ -699,8 +719,9 @@ __device__ __forceinline__ void key_block(float (&dk)[16][4], float (&dv)[16][4]
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int col = 8 * n + 2 * c + e;
-      const float4 x = row[col];  // lse log2(e), D 2^b, b
-      const float ei = ex2_approx(bm - x.z + kPUp), Dn = x.y * am2;  // a whole exponent: exact
+      const float4 x = row[col];  // lse log2(e), b, D 2^(b + a) and its a, at least am
+      // whole exponents: exact
+      const float ei = ex2_approx(bm - x.y + kPUp), Dn = x.z * ex2_approx(am - x.w - kPUp);
 #pragma unroll
       for (int rr = 0; rr < 2; ++rr) {
         const int i = 2 * rr + e;
@@ -832,7 +853,7 @@ __global__ void __launch_bounds__(32 * kSWarps, 1) sink_bwd_sink_kernel(const Si
     __syncwarp();
     const int i0 = first + 16 * (u % per);
     key_block(dk, dv, kf, vfrag, smem_u32(sm.q[w][buf]), smem_u32(sm.d[w][buf]), sm.row[w][buf], sc,
-              bm, pow2i(am) * pow2i(-kPUp), fj, k_lane, t_lane, lane, true, [&](int key, int col) {
+              bm, am, fj, k_lane, t_lane, lane, true, [&](int key, int col) {
                 return key >= a.n_sink || key > i0 + col - kWindow;
               });
     __syncwarp();
@@ -842,7 +863,9 @@ __global__ void __launch_bounds__(32 * kSWarps, 1) sink_bwd_sink_kernel(const Si
   // by the warps that wrote none, then by one of them
   float* part = reinterpret_cast<float*>(smem_raw);
   constexpr int kN = kMaxSink * kHeadDim;
-  const float fk = scale2(a.scale * cq, -(bm + am)), fv = scale2(1.0f, -bm - kPUp);
+  const float xk[2] = {-(bm + am), -(bm + am)}, fv = scale2(1.0f, -bm - kPUp);
+  float fk[2];
+  split_scale(dk, a.scale * cq, xk, fk);
 #pragma unroll 1
   for (int half = kSWarps / 2; half >= 1; half >>= 1) {
     __syncthreads();
@@ -882,7 +905,7 @@ __global__ void __launch_bounds__(32 * kSWarps, 1) sink_bwd_sink_kernel(const Si
       for (int rr = 0; rr < 2; ++rr) {
         const int at = (r + 8 * rr) * kHeadDim + 8 * n + 2 * (lane & 3);
         *reinterpret_cast<float2*>(out + at) =
-            make_float2(dk[n][2 * rr] * fk, dk[n][2 * rr + 1] * fk);
+            make_float2(dk[n][2 * rr] * fk[rr], dk[n][2 * rr + 1] * fk[rr]);
         *reinterpret_cast<float2*>(out + kN + at) =
             make_float2(dv[n][2 * rr] * fv, dv[n][2 * rr + 1] * fv);
       }
@@ -989,7 +1012,6 @@ __global__ void __launch_bounds__(kKThreads, 2) sink_bwd_k_kernel(const SinkBwdA
     for (; issued < min(total, kKStages); ++issued) issue(issued);
   const uint32_t va = smem_u32(sm.v) + 16 * w * kRowBytes + t_lane;
   auto vfrag = [&](int kk, uint32_t (&f)[4]) { ldsm_x4(va ^ (kk << 5), f); };
-  const float am2 = pow2i(am) * pow2i(-kPUp);
   float dk[16][4], dv[16][4];
 #pragma unroll
   for (int n = 0; n < 16; ++n) {
@@ -1008,7 +1030,7 @@ __global__ void __launch_bounds__(kKThreads, 2) sink_bwd_k_kernel(const SinkBwdA
       const int dist = (q0 >> 4) + x - w;  // blocks from this warp's keys to the queries
       if (dist < 0 || dist > 8) continue;
       key_block(dk, dv, kf, vfrag, smem_u32(sm.q[s]) + 16 * x * kRowBytes,
-                smem_u32(sm.d[s]) + 16 * x * kRowBytes, sm.row[s] + 16 * x, sc, bm, am2, fj, k_lane,
+                smem_u32(sm.d[s]) + 16 * x * kRowBytes, sm.row[s] + 16 * x, sc, bm, am, fj, k_lane,
                 t_lane, lane, dist == 0 || dist == 8, [&](int key, int col) {
                   return (dist == 0 && col < key) || (dist == 8 && col >= key);
                 });
@@ -1038,7 +1060,9 @@ __global__ void __launch_bounds__(kKThreads, 2) sink_bwd_k_kernel(const SinkBwdA
   const int rows = min(16, a.T - j0);
   rope_fetch(sm.rope[w], a.k + raw, stride, rows, lane);
   // ---- true scale; the sinks' sums from the queries beyond the window
-  const float fk = scale2(a.scale * cq, -(bm + am)), fv = scale2(1.0f, -bm - kPUp);
+  const float xk[2] = {-(bm + am), -(bm + am)}, fv = scale2(1.0f, -bm - kPUp);
+  float fk[2];
+  split_scale(dk, a.scale * cq, xk, fk);
   const bool add = a.n_sink > 0 && tile == 0 && w == 0;
   const float* sk = a.sink_sum + chain * 2 * kMaxSink * kHeadDim;
 #pragma unroll
@@ -1051,8 +1075,8 @@ __global__ void __launch_bounds__(kKThreads, 2) sink_bwd_k_kernel(const SinkBwdA
         x = *reinterpret_cast<const float2*>(sk + at);
         y = *reinterpret_cast<const float2*>(sk + kMaxSink * kHeadDim + at);
       }
-      dk[n][2 * rr] = fmaf(dk[n][2 * rr], fk, x.x);
-      dk[n][2 * rr + 1] = fmaf(dk[n][2 * rr + 1], fk, x.y);
+      dk[n][2 * rr] = fmaf(dk[n][2 * rr], fk[rr], x.x);
+      dk[n][2 * rr + 1] = fmaf(dk[n][2 * rr + 1], fk[rr], x.y);
       dv[n][2 * rr] = fmaf(dv[n][2 * rr], fv, y.x);
       dv[n][2 * rr + 1] = fmaf(dv[n][2 * rr + 1], fv, y.y);
     }

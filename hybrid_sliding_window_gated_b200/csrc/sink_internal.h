@@ -103,10 +103,10 @@ struct SinkBwdArgs {
   float2* rot;            // [Tp, kMaxPairs]: rot(t w_j)
   uint8_t* kr;            // [B, Hkv, Tp] rows k' / ck, rope order
   uint8_t* vr;            // [B, Hkv, Tp] rows v 2^a, split order
-  float* va;              // [B, Hkv, Tp]: a, the exponent that brings max|v| into [1, 2)
+  float* va;              // [B, Hkv, Tp]: a, the exponent that brings max|v| to 1 .. 4
   uint8_t* qr;            // [B, Hq, Tp] rows q' / cq, rope order
   uint8_t* dr;            // [B, Hq, Tp] rows dA 2^b, split order
-  float4* row;            // [B, Hq, Tp]: lse log2(e), D 2^b, b
+  float4* row;            // [B, Hq, Tp]: lse log2(e), b, D 2^(b + a) and its a
   float* bmin;            // [B, Hq, Tp / 16]: least b of 16 rows
   float* amin;            // [B, Hkv, tiles]: least a of the keys the tile's queries may see
   float* dwq_part;        // [B Hkv tiles head_parts, D]

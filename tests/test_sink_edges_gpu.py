@@ -192,3 +192,21 @@ def test_backward_without_eps(B, T, Hq, Hkv, S):
         if name == "wq":  # sums of u RoPE^-1(dq') with |u| <= 4 and rows' errors of either sign
             bound += 4 * cancelled(x, S) / float(want.norm())
         assert su.rel(got, want) <= bound, name
+
+
+# ------------------------------------------------- magnitudes at bf16's ends
+
+
+@pytest.mark.parametrize("T,v,dO", [(200, 3e38, 1e-3), (70, 3e38, 1e-3), (200, 1.2e38, 1e-30),
+                                    (200, 1e-2, 1.2e38), (333, 3e38, 1e-34)])
+def test_backward_of_the_largest_values(T, v, dO):
+    """v or dO up to the end of bf16's range where the gradients themselves are finite."""
+    x = su.draw(1, T, 2, 1, seed=120, grad=True)
+    gen = torch.Generator().manual_seed(121)
+    for name, top in (("v", v), ("dO", dO)):
+        sign = 2.0 * torch.randint(0, 2, x[name].shape, generator=gen) - 1.0
+        size = 0.25 + 0.75 * torch.rand(x[name].shape, generator=gen)
+        x[name] = (sign * size * top).to(torch.bfloat16)
+    ref = su.sink_gradients(su.args(x), x["dO"], 3, 42, 1e4)
+    assert max(float(r.abs().max()) for r in ref) < 3e38
+    check_backward(x, 3)
