@@ -48,6 +48,11 @@
 // scales leave a product where its row or column index carries them; where an
 // index is summed over, the least exponent of the rows at hand takes their place,
 // and only entries far below the largest lose bits.  |dS| 2^(a + b) <= 2 x 128 x 2 x 4.
+//
+// Values that are not finite.  A masked pair has P = dS = 0, but 0 * inf and 0 * NaN are
+// NaN in a product of tiles: the operand rows hold zeros in such places, and the query's
+// lse (from the forward for q and k, here for dA) or the key's exponent (v) is NaN, which
+// reaches P or dP of exactly the pairs that are visible.
 #include <atomic>
 
 #include "launch.cuh"
@@ -64,6 +69,11 @@ __device__ __forceinline__ float scale_exp(float m) {
   if (!(m > 0.0f)) return kNoScale;
   const int e = static_cast<int>((__float_as_uint(m) >> 23) & 255u) - 127;
   return static_cast<float>(max(-126, min(126, -e)));
+}
+// 2^(am - e - up) for a key whose row has exponent e; NaN for a row that is not finite, whose
+// dP is NaN then for every query that sees it.
+__device__ __forceinline__ float key_factor(float am, float e, float up) {
+  return e == e ? pow2i(fmaxf(fminf(am - e, 0.0f) - up, -126.0f)) : e;
 }
 // v 2^x for whole x in [-252, 252], in two steps
 __device__ __forceinline__ float scale2(float v, float x) {
@@ -147,8 +157,10 @@ __global__ void __launch_bounds__(256) sink_bwd_kv_kernel(const SinkBwdArgs a) {
       uint8_t* kt = stage[warp][0] + (e - (t & 7)) * kRowBytes;
       uint8_t* vt = stage[warp][1] + (e - (t & 7)) * kRowBytes;
       store_k_rows<1>(kt, t & 7, x[e], lane, w_lo, w_hi, w_rest, rot1, eps1);
-      const float ex = scale_exp(m[e]);
-      store_v_row(vt, t & 7, v[e], lane, pow2i(ex));
+      // a row that is not finite: zeros, and NaN for its exponent
+      const bool bad = m[e] == INFINITY;
+      const float ex = bad ? NAN : scale_exp(m[e]);
+      store_v_row(vt, t & 7, bad ? make_uint2(0u, 0u) : v[e], lane, bad ? 1.0f : pow2i(ex));
       if (lane == 0 && h0 + e < a.Hkv)
         a.va[(static_cast<long long>(b) * a.Hkv + h0 + e) * a.Tp + t] = ex;
     }
@@ -264,10 +276,15 @@ __global__ void __launch_bounds__(256, 4) sink_bwd_rows_kernel(const SinkBwdArgs
         *reinterpret_cast<uint2*>(
             a.dg + ((static_cast<long long>(b) * a.T + t) * a.Hq + hq) * kHeadDim + 4 * lane) =
             make_uint2(pack_bf16x2(y0.x, y0.y), pack_bf16x2(y1.x, y1.y));
-      const float mx = fmaxf(fmaxf(fabsf(u0[e].x), fabsf(u0[e].y)),
-                             fmaxf(fabsf(u1[e].x), fabsf(u1[e].y)));
-      // magnitudes order as their bits do
-      m[e] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+      // magnitudes order as their bits do, NaN above all
+      const uint32_t mx = max(max(__float_as_uint(fabsf(u0[e].x)), __float_as_uint(fabsf(u0[e].y))),
+                              max(__float_as_uint(fabsf(u1[e].x)), __float_as_uint(fabsf(u1[e].y))));
+      m[e] = __uint_as_float(__reduce_max_sync(0xffffffffu, mx));
+      if (!(m[e] < INFINITY)) {  // a row that is not finite: zeros, and an lse of NaN
+        u0[e] = u1[e] = make_float2(0.f, 0.f);
+        m[e] = 0.f;
+        l2[e] = NAN;
+      }
     }
     // the stage holds rows i & 7 .. of an eight-row tile
     uint8_t* qt = stage[warp][0] - (i & 7) * kRowBytes;
@@ -519,7 +536,7 @@ __global__ void __launch_bounds__(kQThreads, 2) sink_bwd_q_kernel(const SinkBwdA
     float e = am;
     if (i < kBand && i >= shift) e = a.va[chain * a.Tp + t0 - kWindow + i];
     if (i >= kBand && sinks) e = a.va[chain * a.Tp + i - kBand];
-    sm.vf[i] = pow2i(fmaxf(fminf(am - e, 0.0f), -126.0f));
+    sm.vf[i] = key_factor(am, e, 0.0f);
   }
   if (tid == 0 && part == 0) a.amin[chain * a.tiles + tile] = am;
   const float cq = pow2_ceil(warp_absmax(a.wq, lane)), ck = pow2_ceil(warp_absmax(a.wk, lane));
@@ -818,9 +835,7 @@ __global__ void __launch_bounds__(32 * kSWarps, 1) sink_bwd_sink_kernel(const Si
   auto vfrag = [&](int kk, uint32_t (&f)[4]) { ldsm_x4(va ^ (kk << 5), f); };
   float fj[2];
 #pragma unroll
-  for (int rr = 0; rr < 2; ++rr)
-    fj[rr] =
-        pow2i(fmaxf(fminf(am - a.va[chain * a.Tp + r + 8 * rr], 0.0f) - kPUp, -126.0f));
+  for (int rr = 0; rr < 2; ++rr) fj[rr] = key_factor(am, a.va[chain * a.Tp + r + 8 * rr], kPUp);
   float dk[16][4], dv[16][4];
 #pragma unroll
   for (int n = 0; n < 16; ++n) {
@@ -996,8 +1011,7 @@ __global__ void __launch_bounds__(kKThreads, 2) sink_bwd_k_kernel(const SinkBwdA
   float fj[2];
 #pragma unroll
   for (int rr = 0; rr < 2; ++rr)
-    fj[rr] =
-        pow2i(fmaxf(fminf(am - a.va[chain * a.Tp + j0 + r + 8 * rr], 0.0f) - kPUp, -126.0f));
+    fj[rr] = key_factor(am, a.va[chain * a.Tp + j0 + r + 8 * rr], kPUp);
   const uint32_t k_lane = (lane & 7) * kRowBytes + (lane >> 4) * 8 * kRowBytes +
                           ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
   const uint32_t t_lane = (lane & 7) * kRowBytes + ((lane >> 3) & 1) * 8 * kRowBytes +

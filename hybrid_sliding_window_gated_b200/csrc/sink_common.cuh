@@ -120,6 +120,11 @@ __device__ __forceinline__ void rest_pos(int lane, int* chunk0, int* byte) {
   }
 }
 
+// x, or 0 for what is not a finite fp16 number.  An operand tile holds no such values: a
+// masked pair's 0 x NaN would reach the sums of the rows around it.  Where the pair is
+// visible the row's lse is NaN, and P with it.
+__device__ __forceinline__ float finite(float x) { return fabsf(x) <= 65504.0f ? x : 0.0f; }
+
 // k' / ck of N rows, fp16, in rope order into rows r0 .. of `tile`; w_* are this lane's
 // weights divided by ck, rot its pair's rotation at each row's position.  eps of a row that
 // only fills up a tile is not 0, so that the row's zeros stay zeros.  The rows' chains of
@@ -145,11 +150,11 @@ __device__ __forceinline__ void store_k_rows(uint8_t* tile, int r0, const KRow (
   for (int e = 0; e < N; ++e) {
     const float rinv = rsqrtf(ss[e] * (1.0f / kHeadDim) + eps[e]);
     const float u = bf16_f32(x[e].lo) * rinv * w_lo, v = bf16_f32(x[e].hi) * rinv * w_hi;
-    pair[e] = pack_f16x2(u * rot[e].x - v * rot[e].y, v * rot[e].x + u * rot[e].y);
-    r01[e] = pack_f16x2(bf16_lo(x[e].rest.x) * rinv * w_rest.x,
-                        bf16_hi(x[e].rest.x) * rinv * w_rest.y);
-    r23[e] = pack_f16x2(bf16_lo(x[e].rest.y) * rinv * w_rest.z,
-                        bf16_hi(x[e].rest.y) * rinv * w_rest.w);
+    pair[e] = pack_f16x2(finite(u * rot[e].x - v * rot[e].y), finite(v * rot[e].x + u * rot[e].y));
+    r01[e] = pack_f16x2(finite(bf16_lo(x[e].rest.x) * rinv * w_rest.x),
+                        finite(bf16_hi(x[e].rest.x) * rinv * w_rest.y));
+    r23[e] = pack_f16x2(finite(bf16_lo(x[e].rest.y) * rinv * w_rest.z),
+                        finite(bf16_hi(x[e].rest.y) * rinv * w_rest.w));
   }
   int c0, by;
   rest_pos(lane, &c0, &by);

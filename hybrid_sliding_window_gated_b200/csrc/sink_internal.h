@@ -103,7 +103,7 @@ struct SinkBwdArgs {
   float2* rot;            // [Tp, kMaxPairs]: rot(t w_j)
   uint8_t* kr;            // [B, Hkv, Tp] rows k' / ck, rope order
   uint8_t* vr;            // [B, Hkv, Tp] rows v 2^a, split order
-  float* va;              // [B, Hkv, Tp]: a, the exponent that brings max|v| to 1 .. 4
+  float* va;              // [B, Hkv, Tp]: a, the exponent that brings max|v| to 1 .. 4 (NaN: not finite)
   uint8_t* qr;            // [B, Hq, Tp] rows q' / cq, rope order
   uint8_t* dr;            // [B, Hq, Tp] rows dA 2^b, split order
   float4* row;            // [B, Hq, Tp]: lse log2(e), b, D 2^(b + a) and its a

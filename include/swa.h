@@ -346,11 +346,15 @@ int swa_sink_fwd(const swa_params_t* p, int32_t n_sink, const swa_bf16_t* q, con
  * [B,T,Hq,D] bf16 (where swa_bwd recomputes the attention output) beside its lse, and
  * the upstream gradient dO.  Writes dq, dk, dv, dg (bf16) and ADDS the weight
  * gradients into dwq, dwk [D] (fp32; the caller zeroes them).  Sums are made in a
- * fixed order: equal inputs give equal bits.  Gradients and values of any finite
- * magnitude are carried by power-of-two scales per row; where an index is summed over,
- * entries 2^24 below the largest among the 192 tokens at hand lose bits, so rows
- * behind a padded sequence should hold numbers of ordinary size (and dO = 0): infinities
- * and NaN reach the gradients of the tokens around them.  `workspace`: caller-owned
+ * fixed order: equal inputs give equal bits.  Every row of v and of dA = dO sigmoid(g)
+ * enters in fp16 under a power-of-two scale of its own, so rows may have any finite
+ * magnitude; an entry below 2^-14 of its row's largest loses bits.  So does a row 2^-14
+ * below the largest of those it is summed with or that lie beside them: dq over keys, dk
+ * and dv over queries, in tiles of 64 tokens and up to 512 tokens at a time.  Infinities
+ * and NaN reach the gradients of the rows that a visible pair joins with theirs, and no
+ * others (all gradients of such a row may be NaN), and dwq and dwk, which sum over all
+ * rows.  A query of a padded sequence sees the keys before it: rows behind the last token
+ * should hold numbers of ordinary size, and dO = 0.  `workspace`: caller-owned
  * device scratch of swa_sink_bwd_workspace_size bytes, 256-byte aligned.  Pointers 16-byte
  * aligned; errors as swa_fwd.
  */

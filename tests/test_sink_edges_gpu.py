@@ -210,3 +210,43 @@ def test_backward_of_the_largest_values(T, v, dO):
     ref = su.sink_gradients(su.args(x), x["dO"], 3, 42, 1e4)
     assert max(float(r.abs().max()) for r in ref) < 3e38
     check_backward(x, 3)
+
+
+# -------------------------------------- values that are not finite, backward
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("where", ["k", "k_late", "v", "v_sink", "q", "dO"])
+def test_backward_hides_what_is_masked(where, bad):
+    """A row that is not finite reaches the gradients of the rows that a visible pair
+    joins it with, and no others.  Token 10 is no sink, though it shares the sinks' tile."""
+    T, S, Hq, Hkv = 400, 3, 4, 2
+    x = su.draw(1, T, Hq, Hkv, seed=130, grad=True)
+    clean = {n: t.clone() for n, t in x.items()}
+    name, at, head = {"k": ("k", 10, 0), "k_late": ("k", 390, 1), "v": ("v", 100, 1),
+                      "v_sink": ("v", 2, 0), "q": ("q", 300, 1), "dO": ("dO", 250, 2)}[where]
+    x[name][0, at, head, 5] = bad
+    t, dO = su.args(x, DEV), x["dO"].to(DEV)
+    o, lse = swa.sink_fwd(*t, S, want_lse=True)
+    got = swa.sink_bwd(*t, o, lse, dO, S)
+    ok()
+    want = su.sink_gradients(su.args(clean), clean["dO"], S, 42, 1e4)
+    # queries (by query head) whose probabilities or dP the row enters, then the keys they see
+    kvh = head if name in ("k", "v") else head // (Hq // Hkv)
+    heads = range(2 * kvh, 2 * kvh + 2) if name in ("k", "v") else [head]
+    queries = [i for i in range(T) if at in su.visible(i, S, T)] if name in ("k", "v") else [at]
+    keys = sorted({j for i in queries for j in su.visible(i, S, T)})
+    free = {n: torch.ones_like(x[n], dtype=torch.bool) for n in ("q", "k", "v", "g")}
+    for h in heads:
+        free["q"][0, queries, h] = False
+        free["g"][0, queries, h] = False
+    for n in ("k", "v"):
+        free[n][0, keys, kvh] = False
+    for n, y, ref in zip("qkvg", got, want):
+        f = free[n]
+        assert torch.isfinite(y[f.to(DEV)]).all(), n
+        assert su.rel(y.cpu()[f], ref[f]) <= (REL_DG if n == "g" else REL), n
+    # what a visible pair joins with it is not quietly finite
+    for h in heads:
+        assert (~torch.isfinite(got[0][0, queries, h])).any(dim=-1).all()
+    assert (~torch.isfinite(got[1][0, keys, kvh])).any(dim=-1).all()
