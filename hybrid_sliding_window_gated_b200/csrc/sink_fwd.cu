@@ -21,9 +21,9 @@
 // staging tile one ahead, so its copy does not wait for the ring.
 //
 // Numbers.  All products have fp16 operands and fp32 sums.  q' and k' are divided
-// by a power of two not below the norm weights, so they are at most sqrt(128).  A V
-// row whose largest entry lies in [2^-6, 2^15) is taken as it is; any other is
-// scaled by 2^a into [1, 2), and P carries 2^(a_min - a) then.  P is relative to its
+// by a power of two not below the norm weights, so they are at most sqrt(128).  A V row is
+// scaled by 2^a: by 2^8 where its largest entry lies in [2^-6, 2^7), else to bring that into
+// [2^8, 2^9), and P carries 2^(a_min - a) then.  P is relative to its
 // row's maximum, where it is 2^14 (one pass of TMEM loads; relative to the fixed bound
 // scale D max|wq| max|wk| of the plain forward it would leave fp16's range), and not
 // divided by its row sum before the product.  o is within 1.7e-3 (relative, 2-norm) of
@@ -79,7 +79,7 @@ struct alignas(1024) Smem {
   float2 rot_tile[4][kMaxPairs];
   float wq[kHeadDim], wk[kHeadDim];    // divided by cq, ck
   float va[kRing];                     // a of each V row (v 2^a is stored)
-  int scaled[kSlots + 1];              // some row of the slot (or a sink) has a != 0
+  int scaled[kSlots + 1];              // some row of the slot (or a sink) has a != kVExp
   float cc;                            // cq ck
   uint64_t rotfull[4], runfull, stgfull, stgempty, kready[3], kempty[3];
   uint64_t vfull[3], vready[3], vempty[3];
@@ -809,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float e = v_half_row(sm.v[head], s * kTok + tok, true);
             if (head == 0) sm.va[s * kTok + tok] = e;
             // the slot's flag: set by any of the four warps, cleared by none but the first
-            const bool any = __any_sync(0xffffffffu, e != 0.0f && e != kZeroRow);
+            const bool any = __any_sync(0xffffffffu, e != kVExp && e != kZeroRow);
             if (lane == 0) {
               if (any) atomicOr(&sm.scaled[s], 1 << wq4);
               else atomicAnd(&sm.scaled[s], ~(1 << wq4));
@@ -829,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (wq4 == 0) {  // rows past n_sink become zeros
               const int at = kSlots * kTok + tok;
               const float e = v_half_row(sm.v[head], at, tok < a.n_sink);
-              const bool any = __any_sync(0xffffffffu, e != 0.0f && e != kZeroRow);
+              const bool any = __any_sync(0xffffffffu, e != kVExp && e != kZeroRow);
               if (head == 0) sm.va[at] = e;
               if (lane == 0) sm.scaled[kSlots] = any;
             }
@@ -845,11 +845,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // P is 2^14 at the row's maximum, so that fp16 keeps P down to 2^-28 of it normal.
       const float ms = mx == -INFINITY ? 0.0f : mx * sc - 14.0f;  // all NaN: any reference
       // Least exponent of the V rows that this row sees (what a masked one holds must
-      // not matter).  With V near 1 no row is scaled.
+      // not matter).  With V near 1 it is kVExp for all.
       bool scaled = see_sinks && sm.scaled[kSlots] != 0;
       for (int s = 0; s < kSlots; ++s) scaled = scaled || (dist(s) >= 0 && sm.scaled[s] != 0);
       scaled = __any_sync(0xffffffffu, scaled);  // TMEM loads below: one way for the warp
-      float am = 0.0f;
+      float am = kVExp;
       if (scaled) {
         am = 126.0f;
 #pragma unroll 1
@@ -994,8 +994,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (p == 0.0f || key0 + e >= a.T) continue;
                 const uint16_t* vrow =
                     a.v + ((static_cast<long long>(c.b) * a.T + key0 + e) * a.Hkv + c.kvh) * kHeadDim;
-                float f = 1.0f;
-                if (scaled) {  // P carries 2^-a of its key (the ring's record may have moved on)
+                float f = pow2i(kVExp);
+                if (scaled) {  // the key's own a (the ring's record may have moved on)
                   uint32_t m = 0;
                   for (int i = 0; i < kHeadDim; ++i) m = max(m, vrow[i] & 0x7fffu);
                   f = pow2i(v_exp(__uint_as_float(min(m, 0x7f80u) << 16)));

@@ -328,14 +328,18 @@ int swa_global_decode_step(const swa_params_t* p, const int64_t* pos, const swa_
  * every sequence visible to all later ones.  Query i attends key j when j <= i
  * and (i - j < window or j < n_sink); a sink inside the window counts once.
  * Norm, RoPE (at the tokens' own positions), GQA and gate are those of swa_fwd,
- * and n_sink = 0 is swa_fwd's attention.  0 <= n_sink <= 16 (a negative one
+ * and n_sink = 0 is swa_fwd's formula.  0 <= n_sink <= 16 (a negative one
  * returns SWA_ERR_INVALID_ARG, more than 16 SWA_ERR_UNSUPPORTED).  No
  * counterpart in the pages: a window layer that streams past its window keeps
  * the attention mass that the first tokens draw.
  *
  * swa_sink_fwd: arguments and results of swa_fwd.  A key that a query does not
  * see never reaches its output, whatever it holds (NaN and infinities
- * included), so rows behind a padded sequence may hold anything.
+ * included), so rows behind a padded sequence may hold anything.  q', k' and v enter
+ * in fp16 (swa_fwd's in bf16), v under a power-of-two scale of each row: an entry at
+ * least 2^-19 of its row's largest keeps all its bf16 bits, a smaller one may lose some.
+ * Tiles with a row of v whose largest entry is not in [2^-6, 128) take longer (4 x 4096
+ * tokens of 32 / 8 heads: 384 us where all are such, 225 otherwise).
  */
 int swa_sink_fwd(const swa_params_t* p, int32_t n_sink, const swa_bf16_t* q, const swa_bf16_t* k,
                  const swa_bf16_t* v, const swa_bf16_t* g, const float* wq, const float* wk,

@@ -250,3 +250,25 @@ def test_backward_hides_what_is_masked(where, bad):
     for h in heads:
         assert (~torch.isfinite(got[0][0, queries, h])).any(dim=-1).all()
     assert (~torch.isfinite(got[1][0, keys, kvh])).any(dim=-1).all()
+
+
+# ---------------------------------------- V entries far below their row's own
+
+
+@pytest.mark.parametrize("top", [2.0 ** -6, 1.0, 100.0, 127.0, 3e4, 1e10])
+def test_forward_keeps_small_dims_of_v(top):
+    """Every dim of o by itself, where V's dims differ by up to 2^19 in size: an entry keeps
+    its bf16 bits whatever its row's largest is.  P is off by 2^-11 of an entry, which the
+    bound of a whole row covers for each dim as well."""
+    x = su.draw(1, 300, 2, 1, seed=140)
+    size = top * 2.0 ** (-19.0 * torch.arange(128) / 127)
+    gen = torch.Generator().manual_seed(141)
+    sign = 2.0 * torch.randint(0, 2, (1, 300, 1, 128), generator=gen) - 1.0
+    x["v"] = (sign * size * (0.75 + 0.25 * torch.rand(1, 300, 1, 128, generator=gen))).to(
+        torch.bfloat16)
+    x["v"][..., 0] = (sign[..., 0] * top).to(torch.bfloat16)
+    o, _ = forward(x, 4)
+    ok()
+    o_ref, _ = su.sink_forward(*su.args(x, dtype=torch.float64), 4, 42, 1e4)
+    d = (o.double().cpu() - o_ref).norm(dim=1) / o_ref.norm(dim=1)
+    assert d.max() <= REL, d.max()
