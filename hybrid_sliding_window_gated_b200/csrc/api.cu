@@ -795,6 +795,7 @@ int swa_sink_bwd(const swa_params_t* p, int32_t n_sink, const swa_bf16_t* q, con
   a.G = p->Hq / p->Hkv;
   a.n_sink = n_sink;
   a.half_rot = p->rot_dim / 2;
+  a.flags = p->flags;
   a.chunk = sink_chunk(p->T);
   a.chunks = n_sink > 0 ? (a.Tp + a.chunk - 1) / a.chunk : 0;
   a.head_parts = sink_head_parts(static_cast<long long>(p->B) * p->Hkv * a.tiles, a.G);

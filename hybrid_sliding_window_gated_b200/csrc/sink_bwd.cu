@@ -481,13 +481,13 @@ struct alignas(1024) QSmem {
   float vf[kBand + kMaxSink];  // 2^(amin - a) of each key row
   float dw[4][kHeadDim];
   uint8_t rope[4][kRopeBytes];
-  uint64_t full;
+  uint64_t full, never;
   int abort;
 };
 
 static_assert(sizeof(QSmem) <= 115712, "two CTAs per SM");
 
-enum BwdSite { kSiteBQ = 0xF0, kSiteBFull, kSiteBEmpty, kSiteBTile };
+enum BwdSite { kSiteBForced = 0xF0, kSiteBFull, kSiteBEmpty, kSiteBTile };
 
 // One CTA per (batch row, KV head, 64 queries), or per part of the head's query heads
 // where those are too few for the SMs (sink_head_parts).
@@ -507,6 +507,7 @@ __global__ void __launch_bounds__(kQThreads, 2) sink_bwd_q_kernel(const SinkBwdA
   const int shift = s0 - (t0 - kWindow);    // rows of the band before the sequence
   if (tid == 0) {
     mbar_init(&sm.full, 1);
+    mbar_init(&sm.never, 1);
     sm.abort = 0;
     fence_barrier_init();
   }
@@ -543,8 +544,14 @@ __global__ void __launch_bounds__(kQThreads, 2) sink_bwd_q_kernel(const SinkBwdA
   const float sc = a.scale_log2 * cq * ck;
   volatile int* abort = &sm.abort;
   __syncthreads();
-  const bool ok = __all_sync(0xffffffffu, mbar_wait(&sm.full, 0, abort, a.err, kSiteBFull));
-  if (!ok) return;
+  bool ok = true;
+  if (a.flags & SWA_FLAG_FORCE_TIMEOUT) ok = mbar_wait(&sm.never, 0, abort, a.err, kSiteBForced);
+  ok = __all_sync(0xffffffffu, ok && mbar_wait(&sm.full, 0, abort, a.err, kSiteBFull));
+  if (!ok) {  // copies in flight land before the CTA ends
+    if (tid == 0) mbar_wait_drain(&sm.full, 0);
+    __syncthreads();  // the one at the end, for warps whose wait did not run out
+    return;
+  }
 
   const uint32_t k_lane = (lane & 7) * kRowBytes + (lane >> 4) * 8 * kRowBytes +
                           ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
@@ -954,7 +961,7 @@ struct alignas(1024) KSmem {
   float4 row[kKStages][kStageRows];
   float dw[4][kHeadDim];
   uint8_t rope[4][kRopeBytes];
-  uint64_t full[kKStages], empty[kKStages], tile;
+  uint64_t full[kKStages], empty[kKStages], tile, never;
   int abort;
 };
 static_assert(sizeof(KSmem) <= 115712, "two CTAs per SM");
@@ -978,6 +985,7 @@ __global__ void __launch_bounds__(kKThreads, 2) sink_bwd_k_kernel(const SinkBwdA
       mbar_init(&sm.empty[i], 4);
     }
     mbar_init(&sm.tile, 1);
+    mbar_init(&sm.never, 1);
     sm.abort = 0;
     fence_barrier_init();
   }
@@ -1016,7 +1024,9 @@ __global__ void __launch_bounds__(kKThreads, 2) sink_bwd_k_kernel(const SinkBwdA
                           ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
   const uint32_t t_lane = (lane & 7) * kRowBytes + ((lane >> 3) & 1) * 8 * kRowBytes +
                           (((lane >> 4) ^ (lane & 7)) << 4);
-  bool ok = __all_sync(0xffffffffu, mbar_wait(&sm.tile, 0, abort, a.err, kSiteBTile));
+  bool ok = true;
+  if (a.flags & SWA_FLAG_FORCE_TIMEOUT) ok = mbar_wait(&sm.never, 0, abort, a.err, kSiteBForced);
+  ok = __all_sync(0xffffffffu, ok && mbar_wait(&sm.tile, 0, abort, a.err, kSiteBTile));
   uint32_t kf[8][4];
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk)
@@ -1061,11 +1071,14 @@ __global__ void __launch_bounds__(kKThreads, 2) sink_bwd_k_kernel(const SinkBwdA
     __syncwarp();
   }
   if (!ok) {  // copies in flight land before the CTA ends
-    if (tid == 0)
+    if (tid == 0) {
+      mbar_wait_drain(&sm.tile, 0);
       for (int s = 0; s < kKStages; ++s) {
         const int n = (issued - s + kKStages - 1) / kKStages;
         if (n > 0) mbar_wait_drain(&sm.full[s], (n - 1) & 1);
       }
+    }
+    __syncthreads();  // the one at the end, for warps whose waits did not run out
     return;
   }
   const long long raw = ((static_cast<long long>(b) * a.T + min(j0, a.T - 1)) * a.Hkv + kvh) *

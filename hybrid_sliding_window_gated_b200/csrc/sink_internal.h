@@ -81,6 +81,7 @@ struct SinkBwdArgs {
   int n_sink;
   int half_rot;
   int tiles;              // kSinkTile-token tiles per sequence
+  int flags;
   int chunk, chunks;      // the sinks' pass: tokens per CTA, CTAs per (batch row, KV head)
   int head_parts;         // CTAs of the query-major pass per (KV head, tile)
   float scale, scale_log2, eps;

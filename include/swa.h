@@ -71,11 +71,11 @@ enum {
 };
 
 /* Debug bits for swa_params_t.flags (0 in normal use).  FORCE_TIMEOUT makes
- * the kernels of swa_fwd, swa_bwd, swa_decode_step, swa_sink_fwd,
- * swa_sink_decode_step and of swa_global_decode_shared's prefix part wait on a
- * barrier that nothing completes, so tests can check that the bounded wait ends
- * the kernel (its copies drained, TMEM freed) and reports
- * SWA_ERR_DEVICE_TIMEOUT. */
+ * the kernels of swa_fwd, swa_bwd, swa_decode_step, swa_sink_fwd, swa_sink_bwd
+ * (its two product passes), swa_sink_decode_step and of
+ * swa_global_decode_shared's prefix part wait on a barrier that nothing
+ * completes, so tests can check that the bounded wait ends the kernel (its
+ * copies drained, TMEM freed) and reports SWA_ERR_DEVICE_TIMEOUT. */
 enum { SWA_FLAG_FORCE_TIMEOUT = 1 };
 
 typedef struct swa_params {

@@ -272,3 +272,16 @@ def test_forward_keeps_small_dims_of_v(top):
     o_ref, _ = su.sink_forward(*su.args(x, dtype=torch.float64), 4, 42, 1e4)
     d = (o.double().cpu() - o_ref).norm(dim=1) / o_ref.norm(dim=1)
     assert d.max() <= REL, d.max()
+
+
+# ------------------------------------------------------- waits that run out
+
+
+def test_backward_forced_timeout_is_reported_and_context_survives():
+    x = su.draw(1, 200, 2, 1, seed=180, grad=True)
+    t, dO = su.args(x, DEV), x["dO"].to(DEV)
+    o, lse = swa.sink_fwd(*t, 4, want_lse=True)
+    swa.sink_bwd(*t, o, lse, dO, 4, flags=swa.FLAG_FORCE_TIMEOUT)
+    assert swa.get_last_device_error()[0] == swa.ERR_DEVICE_TIMEOUT
+    check_backward(x, 4)
+    check_forward(x, 4)
