@@ -170,6 +170,7 @@ def _need(where, device, **tensors):
     must be a contiguous CUDA tensor on `device` with the dtype and at least
     that many elements; the kernels take its pointer and the sizes in the
     parameter block, so anything else would be misread or overrun."""
+    _on_current_device(where, device)
     index = device.index
     try:
         for t, dtype, n in tensors.values():  # one pass; a call in order ends here
@@ -560,7 +561,6 @@ def sink_fwd(q, k, v, g, wq, wk, n_sink, *, window=128, rot_dim=42, rope_base=1e
     nq, nk = B * T * Hq * D, B * T * Hkv * D
     bf, f32 = torch.bfloat16, torch.float32
     opt = {} if lse is None else {"lse": (lse, f32, B * Hq * T)}
-    _on_current_device("swa_sink_fwd", q.device)
     _need("swa_sink_fwd", q.device, q=(q, bf, nq), k=(k, bf, nk), v=(v, bf, nk), g=(g, bf, nq),
           wq=(wq, f32, D if nq else 0), wk=(wk, f32, D if nq else 0), out=(out, bf, nq), **opt)
     rc = lib().swa_sink_fwd(ctypes.byref(p), n_sink, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(wq),
@@ -588,7 +588,6 @@ def sink_bwd(q, k, v, g, wq, wk, o, lse, dO, n_sink, *, window=128, rot_dim=42, 
     nbytes = int(lib().swa_sink_bwd_workspace_size(ctypes.byref(p), n_sink))
     if workspace is None:
         workspace = _scratch(stream, q.device, nbytes)
-    _on_current_device("swa_sink_bwd", q.device)
     _need_bwd("swa_sink_bwd", q, k, v, g, wq, wk, lse, dO, grads,
               o=(o, torch.bfloat16, B * T * Hq * D), workspace=(workspace, torch.uint8, nbytes))
     rc = lib().swa_sink_bwd(ctypes.byref(p), n_sink, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(wq),
@@ -613,7 +612,6 @@ def sink_decode_step(pos, q, k_new, v_new, g, wq, wk, k_cache, v_cache, k_sink, 
                     eps=eps, scale=scale, flags=flags)
     nq, nk = N * Hq * D, N * Hkv * D
     bf, f32 = torch.bfloat16, torch.float32
-    _on_current_device("swa_sink_decode_step", q.device)
     _need("swa_sink_decode_step", q.device, pos=(pos, torch.int64, N), q=(q, bf, nq),
           k_new=(k_new, bf, nk), v_new=(v_new, bf, nk), g=(g, bf, nq),
           wq=(wq, f32, D if N else 0), wk=(wk, f32, D if N else 0),
@@ -640,7 +638,6 @@ def prefill_to_sinks(k, v, wk, k_sink, v_sink, starts=None, lens=None, pos0=None
     nk = (B if lens is None else 1) * T * Hkv * D if n else 0
     extra = {name: (t, i64, B) for name, t in (("starts", starts), ("lens", lens), ("pos0", pos0))
              if t is not None}
-    _on_current_device("swa_prefill_to_sinks", k_sink.device)
     _need("swa_prefill_to_sinks", k_sink.device, k=(k, bf, nk), v=(v, bf, nk),
           wk=(wk, torch.float32, D if n else 0), k_sink=(k_sink, bf, n), v_sink=(v_sink, bf, n),
           **extra)
@@ -678,7 +675,6 @@ def global_decode_shared(pos, q, k_new, v_new, wq, wk, k_prefix, v_prefix, prefi
     nq, nk = N * Hq * D, N * Hkv * D
     npre = Hkv * pcap * D if N and prefix_len else 0
     bf, f32 = torch.bfloat16, torch.float32
-    _on_current_device("swa_global_decode_shared", q.device)
     _need("swa_global_decode_shared", q.device, pos=(pos, torch.int64, N), q=(q, bf, nq),
           k_new=(k_new, bf, nk), v_new=(v_new, bf, nk), wq=(wq, f32, D if N else 0),
           wk=(wk, f32, D if N else 0), k_prefix=(k_prefix, bf, npre), v_prefix=(v_prefix, bf, npre),
