@@ -602,21 +602,23 @@ def sink_decode_step(pos, q, k_new, v_new, g, wq, wk, k_cache, v_cache, k_sink, 
                      rot_dim=42, rope_base=1e7, eps=1e-6, scale=0.0, out=None, flags=0,
                      stream=None):
     """:func:`decode_step` with sinks (swa_sink_decode_step): k_sink, v_sink
-    [N,Hkv,n_sink,128] bf16 hold k', v of positions 0 .. n_sink-1 and are updated
-    in place, as are the rings; returns o [N,Hq,128]."""
+    [N,Hkv,n_sink,128] bf16 (or both None: no sinks) hold k', v of positions
+    0 .. n_sink-1 and are updated in place, as are the rings; returns o [N,Hq,128]."""
     N, Hq, D = q.shape
-    Hkv, W, S = k_cache.shape[1], k_cache.shape[2], k_sink.shape[2]
+    Hkv, W = k_cache.shape[1], k_cache.shape[2]
+    S = 0 if k_sink is None else k_sink.shape[2]
     if out is None:
         out = _new(stream, torch.empty_like, q, device=q.device)
     p = make_params(N, 1, Hq, Hkv, head_dim=D, window=W, rot_dim=rot_dim, rope_base=rope_base,
                     eps=eps, scale=scale, flags=flags)
     nq, nk = N * Hq * D, N * Hkv * D
     bf, f32 = torch.bfloat16, torch.float32
+    sinks = {} if k_sink is None and v_sink is None else {
+        "k_sink": (k_sink, bf, nk * S), "v_sink": (v_sink, bf, nk * S)}
     _need("swa_sink_decode_step", q.device, pos=(pos, torch.int64, N), q=(q, bf, nq),
           k_new=(k_new, bf, nk), v_new=(v_new, bf, nk), g=(g, bf, nq),
           wq=(wq, f32, D if N else 0), wk=(wk, f32, D if N else 0),
-          k_cache=(k_cache, bf, nk * W), v_cache=(v_cache, bf, nk * W),
-          k_sink=(k_sink, bf, nk * S), v_sink=(v_sink, bf, nk * S), out=(out, bf, nq))
+          k_cache=(k_cache, bf, nk * W), v_cache=(v_cache, bf, nk * W), out=(out, bf, nq), **sinks)
     rc = lib().swa_sink_decode_step(ctypes.byref(p), S, _ptr(pos), _ptr(q), _ptr(k_new),
                                     _ptr(v_new), _ptr(g), _ptr(wq), _ptr(wk), _ptr(k_cache),
                                     _ptr(v_cache), _ptr(k_sink), _ptr(v_sink), _ptr(out),

@@ -85,3 +85,28 @@ def test_tensors_on_another_device_than_the_current_one(name, monkeypatch):
     monkeypatch.setattr(swa, "_current_device", lambda: 0)
     CALLS[name](inputs())
     assert len(launched) == 1
+
+
+def launches(monkeypatch, *names):
+    swa_build.build()
+    monkeypatch.setattr(swa, "_current_device", lambda: 0)
+    monkeypatch.setattr(swa, "_stream", lambda s: 0)
+    seen = []
+    for f in names:
+        monkeypatch.setattr(swa.lib(), "swa_" + f, lambda *a: seen.append(a) or 0)
+    return seen
+
+
+def test_decode_step_without_sink_caches(monkeypatch):
+    """No caches, as in the C call, are no sinks; one without the other is a mistake."""
+    seen = launches(monkeypatch, "sink_decode_step")
+    x = inputs()
+    call = lambda ks, vs: swa.sink_decode_step(x.pos, x.one, x.new, x.new, x.one, x.w, x.w, x.ring,
+                                               x.ring, ks, vs, out=x.one)
+    call(None, None)
+    assert seen[0][1] == 0 and seen[0][11] is None and seen[0][12] is None
+    c = types.SimpleNamespace(**{n: torch.zeros(t.shape, dtype=t.dtype) for n, t in vars(x).items()
+                                 if n in ("pos", "one", "new", "w", "ring", "k")})
+    for pair in ((c.k, None), (None, c.k)):
+        with pytest.raises(TypeError, match="_sink must be a torch.Tensor"):
+            swa.sink_decode_step(c.pos, c.one, c.new, c.new, c.one, c.w, c.w, c.ring, c.ring, *pair)

@@ -285,3 +285,17 @@ def test_backward_forced_timeout_is_reported_and_context_survives():
     assert swa.get_last_device_error()[0] == swa.ERR_DEVICE_TIMEOUT
     check_backward(x, 4)
     check_forward(x, 4)
+
+
+# ------------------------------------------------------- no sink caches
+
+
+def test_decode_without_sink_caches_is_the_step_with_empty_ones():
+    y, caches = decode_inputs(5, 4, 2, 0, seed=190)
+    y, caches = [z.to(DEV) for z in y], [c.to(DEV) for c in caches]
+    pos = torch.tensor([0, 3, 127, 128, 1000], device=DEV)
+    rings = [c.clone() for c in caches[:2]]
+    want = swa.sink_decode_step(pos, *y, *caches)
+    assert torch.equal(swa.sink_decode_step(pos, *y, *rings, None, None), want)
+    assert all(torch.equal(a, b) for a, b in zip(rings, caches))
+    ok()
