@@ -200,6 +200,13 @@ def _need(where, device, **tensors):
                              f"the device of the first input")
 
 
+def _alike(where, **caches):
+    """A K cache's sizes lay out the V cache too: one of another capacity would be misread."""
+    (nk, k), (nv, v) = caches.items()
+    if k.numel() != v.numel():
+        raise ValueError(f"{where}: {nk} has {k.numel()} elements, {nv} {v.numel()}")
+
+
 def _on_current_device(where, device):
     """The library launches on the current device, whatever device the tensors are on."""
     if device.type == "cuda" and device.index != _current_device():
@@ -619,6 +626,9 @@ def sink_decode_step(pos, q, k_new, v_new, g, wq, wk, k_cache, v_cache, k_sink, 
           k_new=(k_new, bf, nk), v_new=(v_new, bf, nk), g=(g, bf, nq),
           wq=(wq, f32, D if N else 0), wk=(wk, f32, D if N else 0),
           k_cache=(k_cache, bf, nk * W), v_cache=(v_cache, bf, nk * W), out=(out, bf, nq), **sinks)
+    _alike("swa_sink_decode_step", k_cache=k_cache, v_cache=v_cache)
+    if sinks:
+        _alike("swa_sink_decode_step", k_sink=k_sink, v_sink=v_sink)
     rc = lib().swa_sink_decode_step(ctypes.byref(p), S, _ptr(pos), _ptr(q), _ptr(k_new),
                                     _ptr(v_new), _ptr(g), _ptr(wq), _ptr(wk), _ptr(k_cache),
                                     _ptr(v_cache), _ptr(k_sink), _ptr(v_sink), _ptr(out),
@@ -643,6 +653,7 @@ def prefill_to_sinks(k, v, wk, k_sink, v_sink, starts=None, lens=None, pos0=None
     _need("swa_prefill_to_sinks", k_sink.device, k=(k, bf, nk), v=(v, bf, nk),
           wk=(wk, torch.float32, D if n else 0), k_sink=(k_sink, bf, n), v_sink=(v_sink, bf, n),
           **extra)
+    _alike("swa_prefill_to_sinks", k_sink=k_sink, v_sink=v_sink)
     rc = lib().swa_prefill_to_sinks(ctypes.byref(p), S, _ptr(starts), _ptr(lens), _ptr(pos0),
                                     _ptr(k), _ptr(v), _ptr(wk), _ptr(k_sink), _ptr(v_sink),
                                     _stream(stream))
@@ -666,6 +677,9 @@ def global_decode_shared(pos, q, k_new, v_new, wq, wk, k_prefix, v_prefix, prefi
     Hkv, cap = k_cache.shape[1], k_cache.shape[2]
     if k_prefix.dim() == 4 and k_prefix.shape[0] != 1:
         raise ValueError("swa_global_decode_shared: k_prefix holds more than one sequence")
+    if k_prefix.shape[-3] != Hkv:
+        raise ValueError(f"swa_global_decode_shared: k_prefix has {k_prefix.shape[-3]} heads, "
+                         f"k_cache {Hkv}")
     pcap = k_prefix.shape[-2]
     if out is None:
         out = _new(stream, torch.empty_like, q, device=q.device)
@@ -682,6 +696,8 @@ def global_decode_shared(pos, q, k_new, v_new, wq, wk, k_prefix, v_prefix, prefi
           wk=(wk, f32, D if N else 0), k_prefix=(k_prefix, bf, npre), v_prefix=(v_prefix, bf, npre),
           k_cache=(k_cache, bf, nk * cap), v_cache=(v_cache, bf, nk * cap), out=(out, bf, nq),
           workspace=(workspace, torch.uint8, nbytes if N else 0))
+    _alike("swa_global_decode_shared", k_prefix=k_prefix, v_prefix=v_prefix)
+    _alike("swa_global_decode_shared", k_cache=k_cache, v_cache=v_cache)
     rc = lib().swa_global_decode_shared(ctypes.byref(p), prefix_len, pcap, _ptr(k_prefix),
                                         _ptr(v_prefix), _ptr(pos), _ptr(q), _ptr(k_new),
                                         _ptr(v_new), _ptr(wq), _ptr(wk), _ptr(k_cache),

@@ -110,3 +110,36 @@ def test_decode_step_without_sink_caches(monkeypatch):
     for pair in ((c.k, None), (None, c.k)):
         with pytest.raises(TypeError, match="_sink must be a torch.Tensor"):
             swa.sink_decode_step(c.pos, c.one, c.new, c.new, c.one, c.w, c.w, c.ring, c.ring, *pair)
+
+
+def test_caches_of_unlike_sizes(monkeypatch):
+    """K and V caches of one call share their capacity: the larger one is no valid V cache."""
+    seen = launches(monkeypatch, "sink_decode_step", "prefill_to_sinks", "global_decode_shared")
+    x = inputs()
+    bf = torch.bfloat16
+    sink = [Elsewhere((1, 1, n, 128), bf) for n in (4, 5)]
+    long, wide = Elsewhere((1, 1, 256, 128), bf), Elsewhere((1, 2, 128, 128), bf)
+
+    def decode(vc, vs):
+        swa.sink_decode_step(x.pos, x.one, x.new, x.new, x.one, x.w, x.w, x.ring, vc, sink[0], vs,
+                             out=x.one)
+
+    def shared(kp, vp, vc):
+        swa.global_decode_shared(x.pos, x.one, x.new, x.new, x.w, x.w, kp, vp, 16, x.ring, vc,
+                                 out=x.one, workspace=x.big)
+
+    for match, call in [
+        ("v_cache", lambda: decode(long, sink[0])),
+        ("v_sink", lambda: decode(x.ring, sink[1])),
+        ("v_sink", lambda: swa.prefill_to_sinks(x.k, x.k, x.w, *sink, Hq=2)),
+        ("v_prefix", lambda: shared(x.ring, long, x.ring)),
+        ("v_cache", lambda: shared(x.ring, x.ring, long)),
+        ("2 heads", lambda: shared(wide, wide, x.ring)),
+    ]:
+        with pytest.raises(ValueError, match=match):
+            call()
+    assert not seen
+    decode(x.ring, sink[0])
+    swa.prefill_to_sinks(x.k, x.k, x.w, sink[0], sink[0], Hq=2)
+    shared(x.ring, x.ring, x.ring)
+    assert len(seen) == 3
