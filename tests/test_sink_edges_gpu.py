@@ -274,6 +274,115 @@ def test_forward_keeps_small_dims_of_v(top):
     assert d.max() <= REL, d.max()
 
 
+# ----------------------------------------- the backward's other launch shapes
+
+
+def gathered_forward(q, k, v, g, wq, wk, n_sink, R=42, base=1e4):
+    """su.sink_forward for one sequence, each query's keys gathered at once (64 bits)."""
+    T, Hq, Hkv = q.shape[1], q.shape[2], k.shape[2]
+    dev = q.device
+    cpu = lambda y, w: su.norm_rope(y.cpu(), w.cpu(), torch.arange(T).expand(1, T), R, base).to(dev)
+    qq, kk = cpu(q, wq)[0].reshape(T, Hkv, -1, 128), cpu(k, wk)[0]
+    i = torch.arange(T, device=dev)
+    idx = torch.cat([i[:, None] - torch.arange(127, -1, -1, device=dev),
+                     torch.arange(n_sink, device=dev).expand(T, n_sink)], 1)
+    seen = torch.cat([idx[:, :128] >= 0, idx[:, 128:] <= i[:, None] - 128], 1)
+    idx = idx.clamp_min(0)
+    s = torch.einsum("thgd,tjhd->thgj", qq, kk[idx]) / math.sqrt(128)
+    p = torch.softmax(s.masked_fill(~seen[:, None, None], -math.inf), -1)
+    a = torch.einsum("thgj,tjhd->thgd", p, v[0][idx]).reshape(1, T, Hq, 128)
+    return a * torch.sigmoid(g)
+
+
+def gathered_gradients(x, n_sink):
+    t = [y.double().to(DEV).requires_grad_() for y in su.args(x)]
+    o = gathered_forward(*t, n_sink)
+    return torch.autograd.grad((o * x["dO"].double().to(DEV)).sum(), t)
+
+
+def test_gathered_form_is_the_plain_one():
+    x = su.draw(1, 300, 4, 2, seed=150, grad=True)
+    for a, b in zip(gathered_gradients(x, 5), su.sink_gradients(su.args(x), x["dO"], 5, 42, 1e4)):
+        assert su.rel(a, b) <= 1e-12
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,S", [(4200, 2, 1, 4), (5000, 3, 1, 16), (4097, 4, 2, 0)])
+def test_backward_of_long_sequences(T, Hq, Hkv, S):
+    """More than 4,096 tokens: the sinks' pass in longer chunks."""
+    x = su.draw(1, T, Hq, Hkv, seed=151 + T, grad=True)
+    t = su.args(x, DEV)
+    o, lse = swa.sink_fwd(*t, S, want_lse=True)
+    grads = swa.sink_bwd(*t, o, lse, x["dO"].to(DEV), S)
+    ok()
+    for name, got, want in zip(su.NAMES, grads, gathered_gradients(x, S)):
+        assert su.rel(got, want) <= (REL_DG if name == "g" else REL), name
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,S", [(150, 130, 4, 1, 4), (110, 130, 8, 1, 3),
+                                          (33, 130, 5, 1, 4), (20, 200, 7, 1, 16),
+                                          (30, 65, 10, 2, 2)])
+def test_backward_of_many_sequences(B, T, Hq, Hkv, S):
+    """From one head per CTA of the query-major pass to all of a group in one, and uneven
+    parts between: copies of one sequence get its gradients, dwq and dwk B times its own."""
+    one = su.draw(1, T, Hq, Hkv, seed=160 + B, grad=True)
+    single = check_backward(one, S)
+    rep = lambda y: y.expand(B, *y.shape[1:]).contiguous()
+    x = {n: (y if n in ("wq", "wk") else rep(y)) for n, y in one.items()}
+    t = su.args(x, DEV)
+    o, lse = swa.sink_fwd(*t, S, want_lse=True)
+    grads = swa.sink_bwd(*t, o, lse, x["dO"].to(DEV), S)
+    ok()
+    for a, b in zip(grads[:4], single[:4]):
+        assert torch.equal(a, b.expand_as(a))
+    for a, b in zip(grads[4:], single[4:]):
+        # fp32 sums of at most B x 4 x 128 x 10 terms, 2^-24 each, of random signs
+        assert su.rel(a, B * b.double()) <= 1e-4
+
+
+# -------------------------------------------------------- large norm weights
+
+
+def test_rows_on_one_key_with_large_norm_weights():
+    """Scores in the hundreds.  Each is off by at most e = 2^-10 x 11.4 x 400 x 1.7 = 7.6,
+    so keys that hold 1e-12 of a row together hold at most 1e-12 exp(2 e) = 4e-6 of it."""
+    x = su.draw(1, 260, 2, 1, seed=8)
+    x["wq"], x["wk"] = 20 * x["wq"], 20 * x["wk"]
+    o, _ = forward(x, 4)
+    ok()
+    t = su.args(x, dtype=torch.float64)
+    o_ref, lse = su.sink_forward(*t, 4, 42, 1e4)
+    pos = torch.arange(260).expand(1, 260)
+    q, k = su.norm_rope(t[0], t[4], pos, 42, 1e4)[0], su.norm_rope(t[1], t[5], pos, 42, 1e4)[0, :, 0]
+    rows = 0
+    for i in range(260):
+        s = torch.einsum("hd,jd->hj", q[i], k[su.visible(i, 4, 260)]) / math.sqrt(128)
+        p = torch.exp(s - lse[0, :, i, None])
+        for h in range(2):
+            top = int(p[h].argmax())
+            rest = float(p[h].sum() - p[h, top])
+            if rest > 1e-12:
+                continue
+            rows += 1
+            d = (o[0, i, h].double().cpu() - o_ref[0, i, h]).norm()
+            assert d <= REL * o_ref[0, i, h].norm()
+    assert rows >= 200
+
+
+def test_backward_with_large_norm_weights():
+    """Weights of 3: a score of standard deviation 9 carries the roundings of 128 products
+    of fp16 operands, of about 2e-4 each, so 9 x sqrt(2) x 2e-4 = 2.5e-3, a factor of as
+    much on P and as much again on D: 5e-3 beside REL."""
+    x = su.draw(1, 260, 4, 2, seed=170, grad=True)
+    x["wq"], x["wk"] = 3 * x["wq"], 3 * x["wk"]
+    t = su.args(x, DEV)
+    o, lse = swa.sink_fwd(*t, 4, want_lse=True)
+    grads = swa.sink_bwd(*t, o, lse, x["dO"].to(DEV), 4)
+    ok()
+    ref = su.sink_gradients(su.args(x), x["dO"], 4, 42, 1e4)
+    for name, got, want in zip(su.NAMES, grads, ref):
+        assert su.rel(got, want) <= REL + 5e-3, name
+
+
 # ------------------------------------------------------- waits that run out
 
 
