@@ -999,8 +999,8 @@ __global__ void __launch_bounds__(256) global_combine_kernel(const GlobalDecArgs
           l[e] = __shfl_sync(0xffffffffu, x.y, j0 + e);
           v4[e] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (!(f[e] < 0.0f))  // else no such partial, or one without keys whose O was not written
-            v4[e] = __ldg(reinterpret_cast<const float4*>(
-                part + (first + (c0 + j0 + e) * step) * kHeadDim + 4 * lane));
+            v4[e] = *reinterpret_cast<const float4*>(
+                part + (first + (c0 + j0 + e) * step) * kHeadDim + 4 * lane);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {

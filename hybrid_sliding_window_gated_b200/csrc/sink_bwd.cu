@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(256, 4) sink_bwd_rows_kernel(const SinkBwdArgs
 #pragma unroll
     for (int e = 0; e < kN; ++e) {
       const int t = t0 + i + e;
-      rot[e] = lane < kMaxPairs ? __ldg(a.rot + static_cast<long long>(t) * kMaxPairs + lane)
+      rot[e] = lane < kMaxPairs ? a.rot[static_cast<long long>(t) * kMaxPairs + lane]
                                 : make_float2(1.f, 0.f);
       l2[e] = t < a.T ? __ldg(lse + t) * 1.4426950408889634f : 0.f;
     }
@@ -388,7 +388,7 @@ __device__ __forceinline__ void norm_rope_back(const float (&acc)[16][4], const 
 #pragma unroll
     for (int i = 0; i < 6; ++i) {
       const int j = 8 * (i >> 1) + 2 * c + (i & 1);
-      const float2 cs = __ldg(rot + row * kMaxPairs + j);
+      const float2 cs = rot[row * kMaxPairs + j];
       const float u = acc[2 * (i >> 1)][2 * rr + (i & 1)] * f[rr];
       const float v = acc[2 * (i >> 1) + 1][2 * rr + (i & 1)] * f[rr];
       const float al = u * cs.x + v * cs.y, ah = v * cs.x - u * cs.y;
@@ -576,15 +576,15 @@ __global__ void __launch_bounds__(kQThreads, 2) sink_bwd_q_kernel(const SinkBwdA
     for (int rr = 0; rr < 2; ++rr) {
       const uint8_t* qrow = a.qr + hrow * kRowBytes + 4 * c;
       const uint8_t* drow = a.dr + hrow * kRowBytes + 4 * c;
-      const float4 rec = __ldg(a.row + hrow + r + 8 * rr);
+      const float4 rec = a.row[hrow + r + 8 * rr];
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           qf[kk][2 * hf + rr] =
-              __ldg(reinterpret_cast<const uint32_t*>(qrow + row_off(r + 8 * rr, 2 * kk + hf)));
+              *reinterpret_cast<const uint32_t*>(qrow + row_off(r + 8 * rr, 2 * kk + hf));
           df[kk][2 * hf + rr] =
-              __ldg(reinterpret_cast<const uint32_t*>(drow + row_off(r + 8 * rr, 2 * kk + hf)));
+              *reinterpret_cast<const uint32_t*>(drow + row_off(r + 8 * rr, 2 * kk + hf));
         }
       L2[rr] = rec.x;
       fs[rr] = -(rec.y + am);
@@ -824,7 +824,7 @@ __global__ void __launch_bounds__(32 * kSWarps, 1) sink_bwd_sink_kernel(const Si
     const int at = i & (kSinkBytes / 16 - 1);
     const uint8_t* src = (i < kSinkBytes / 16 ? a.kr : a.vr) + chain * a.Tp * kRowBytes;
     *reinterpret_cast<uint4*>((i < kSinkBytes / 16 ? sm.ks : sm.vs) + 16 * at) =
-        __ldg(reinterpret_cast<const uint4*>(src + 16 * at));
+        *reinterpret_cast<const uint4*>(src + 16 * at);
   }
   float bm, am;
   tile_scales(a, b, kvh, ta / kSinkTile, tb / kSinkTile, lane, &bm, &am);
