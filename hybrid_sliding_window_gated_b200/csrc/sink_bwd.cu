@@ -11,8 +11,9 @@
 //   dv_j  = sum_i P_ij dA_i
 // and from dx' (x = q or k) back through RoPE and the norm, with u = x / rms:
 //   du = w RoPE^-1(dx'),  dx = (du - u mean(du u)) / rms,  dw = sum RoPE^-1(dx') u.
-// o is the forward's bf16 output: it gives dg without a second P V.  D could come
-// from o too, but dP - D cancels where a row's probability sits on few keys (a
+// o is the forward's bf16 output: it gives dg without a second P V, at the price of its
+// rounding beside dg's own (2.4e-3 in the 2-norm, 1.7e-3 from a recomputed A).  D could
+// come from o too, but dP - D cancels where a row's probability sits on few keys (a
 // sequence's first tokens), and o's rounding would remain.
 //
 // Kernels, each waiting for the one before it on the stream:
@@ -44,7 +45,7 @@
 // Numbers.  All products have fp16 operands and fp32 sums.  q' and k' are divided
 // by a power of two not below the norm weights (at most sqrt(128) then); a row
 // of dA is scaled by 2^b and one of v by 2^a so that its largest entry lies in
-// [1, 4): gradients and values of any magnitude keep fp16's 2^-12 rounding.  The
+// [1, 4): gradients and values of any magnitude keep fp16's 2^-11 rounding.  The
 // scales leave a product where its row or column index carries them; where an
 // index is summed over, the least exponent of the rows at hand takes their place,
 // and only entries far below the largest lose bits.  |dS| 2^(a + b) <= 2 x 128 x 2 x 4.
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(256, 4) sink_bwd_rows_kernel(const SinkBwdArgs
     }
     __syncwarp();  // the rows have landed, and the stage has been read out
     float2 u0[kN], u1[kN];
-    float m[kN], eps[kN];
+    float m[kN], eps[kN], D[kN];
     KRow x[kN];
 #pragma unroll
     for (int e = 0; e < kN; ++e) {
@@ -269,7 +270,9 @@ __global__ void __launch_bounds__(256, 4) sink_bwd_rows_kernel(const SinkBwdArgs
       const float2 q1 = make_float2(bf16_lo(o2.y), bf16_hi(o2.y));
       u0[e] = __fmul2_rn(d0, s0);
       u1[e] = __fmul2_rn(d1, s1);
-      const float2 y0 = __fmul2_rn(__fmul2_rn(d0, q0), n0), y1 = __fmul2_rn(__fmul2_rn(d1, q1), n1);
+      const float2 x0 = __fmul2_rn(d0, q0), x1 = __fmul2_rn(d1, q1);
+      D[e] = (x0.x + x0.y) + (x1.x + x1.y);
+      const float2 y0 = __fmul2_rn(x0, n0), y1 = __fmul2_rn(x1, n1);
       const int t = t0 + i + e;
       eps[e] = t < a.T ? a.eps : 1.0f;
       if (t < a.T)
@@ -286,6 +289,10 @@ __global__ void __launch_bounds__(256, 4) sink_bwd_rows_kernel(const SinkBwdArgs
         l2[e] = NAN;
       }
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int e = 0; e < kN; ++e) D[e] += __shfl_xor_sync(0xffffffffu, D[e], o);
     // the stage holds rows i & 7 .. of an eight-row tile
     uint8_t* qt = stage[warp][0] - (i & 7) * kRowBytes;
     uint8_t* dt = stage[warp][1] - (i & 7) * kRowBytes;
@@ -300,7 +307,8 @@ __global__ void __launch_bounds__(256, 4) sink_bwd_rows_kernel(const SinkBwdArgs
           pack_f16x2(u0[e].x * f, u0[e].y * f);
       *reinterpret_cast<uint32_t*>(dt + row_off(r, 4 * md + q + 1) + 4 * c) =
           pack_f16x2(u1[e].x * f, u1[e].y * f);
-      if (lane == 0) a.row[out + i + e] = make_float4(l2[e], be, 0.f, 0.f);
+      if (lane == 0)
+        a.row[out + i + e] = make_float4(l2[e], be, fabsf(D[e]) < INFINITY ? D[e] : 0.f, 0.f);
     }
     if (i + kN < 16) fetch_row(i + kN);
     __syncwarp();
@@ -568,7 +576,7 @@ __global__ void __launch_bounds__(kQThreads, 2) sink_bwd_q_kernel(const SinkBwdA
     const long long hrow = (static_cast<long long>(b) * a.Hq + hq) * a.Tp + i0;
     // ---- q' and dA as A fragments: words c of the rows' chunks
     uint32_t qf[8][4], df[8][4];
-    float L2[2], fs[2], Dn[2];
+    float L2[2], fs[2], Dn[2], mid[2];
     const long long raw = ((static_cast<long long>(b) * a.T + min(i0, a.T - 1)) * a.Hq + hq) *
                           kHeadDim;
     rope_fetch(sm.rope[w], a.q + raw, stride, rows, lane);
@@ -588,6 +596,7 @@ __global__ void __launch_bounds__(kQThreads, 2) sink_bwd_q_kernel(const SinkBwdA
         }
       L2[rr] = rec.x;
       fs[rr] = -(rec.y + am);
+      mid[rr] = scale2(rec.z, rec.y + am);
     }
     // the next head's rows, and this one's raw q for the end, towards L2
     {
@@ -599,8 +608,10 @@ __global__ void __launch_bounds__(kQThreads, 2) sink_bwd_q_kernel(const SinkBwdA
       asm volatile("prefetch.global.L2 [%0];" ::"l"(
           a.q + ((static_cast<long long>(b) * a.T + t) * a.Hq + hq) * kHeadDim + 64 * (lane & 1)));
     }
-    // ---- S and dP of all blocks; P and dP stay in registers (fp16) until D, the
-    // sum of their products, is known
+    // ---- S and dP of all blocks; P and dP - mid stay in registers (fp16) until D, the
+    // sum of P dP, is known.  mid is D from the forward's o, as exact as its rounding
+    // allows: where a row's probability sits on few keys their dP is near D, and dP itself
+    // in fp16 would leave 2^-11 of it in the difference.
     uint32_t pf[10][4], gf[10][4];
     Dn[0] = Dn[1] = 0.f;
 #pragma unroll
@@ -646,8 +657,8 @@ __global__ void __launch_bounds__(kQThreads, 2) sink_bwd_q_kernel(const SinkBwdA
           }
           pf[x][2 * n] = pack_f16x2(p[0], p[1]);
           pf[x][2 * n + 1] = pack_f16x2(p[2], p[3]);
-          gf[x][2 * n] = pack_f16x2(y[0], y[1]);
-          gf[x][2 * n + 1] = pack_f16x2(y[2], y[3]);
+          gf[x][2 * n] = pack_f16x2(y[0] - mid[0], y[1] - mid[0]);
+          gf[x][2 * n + 1] = pack_f16x2(y[2] - mid[1], y[3] - mid[1]);
           Dn[0] += p[0] * y[0] + p[1] * y[1];
           Dn[1] += p[2] * y[2] + p[3] * y[3];
         }
@@ -662,6 +673,7 @@ __global__ void __launch_bounds__(kQThreads, 2) sink_bwd_q_kernel(const SinkBwdA
       Dn[rr] += __shfl_xor_sync(0xffffffffu, Dn[rr], 2);
       if (c == 0)
         reinterpret_cast<float2*>(a.row + hrow + r + 8 * rr)[1] = make_float2(Dn[rr], am);
+      Dn[rr] -= mid[rr];
     }
     // ---- dQ = dS K', dS = P (dP - D)
     float dq[16][4];

@@ -107,7 +107,7 @@ struct SinkBwdArgs {
   float* va;              // [B, Hkv, Tp]: a, the exponent that brings max|v| to 1 .. 4 (NaN: not finite)
   uint8_t* qr;            // [B, Hq, Tp] rows q' / cq, rope order
   uint8_t* dr;            // [B, Hq, Tp] rows dA 2^b, split order
-  float4* row;            // [B, Hq, Tp]: lse log2(e), b, D 2^(b + a) and its a
+  float4* row;            // [B, Hq, Tp]: lse log2(e), b, then D (from o; later D 2^(b + a), a)
   float* bmin;            // [B, Hq, Tp / 16]: least b of 16 rows
   float* amin;            // [B, Hkv, tiles]: least a of the keys the tile's queries may see
   float* dwq_part;        // [B Hkv tiles head_parts, D]
