@@ -323,19 +323,11 @@ __device__ __forceinline__ uint16_t* da_tile(const BwdArgs& a, int b, int hq, in
   return a.ws_da + ((static_cast<long long>(b) * a.Hq + hq) * a.tiles_per_chain + t) *
                        (kTileBytes / 2);
 }
-// 1-D bulk copies (16-byte aligned, sizes multiples of 16).
+// 1-D bulk copy shared -> global (16-byte aligned, size a multiple of 16).
 __device__ __forceinline__ void bulk_store(void* gdst, const void* ssrc, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(gdst),
                "r"(smem_u32(ssrc)), "r"(bytes)
                : "memory");
-}
-__device__ __forceinline__ void bulk_load(void* sdst, const void* gsrc, uint32_t bytes,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(smem_u32(sdst)),
-      "l"(gsrc), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
 }
 
 // K-major descriptor of k-step kk over both slots of a ring (256 rows).

@@ -74,17 +74,6 @@ __device__ __forceinline__ uint32_t ring_off(int s, int c) {
   return static_cast<uint32_t>((c >> 3) * kHalfBytes + s * 128 + (((c & 7) ^ (s & 7)) << 4));
 }
 
-// 1-D bulk copy global -> shared, completing on `bar` (16-byte aligned, size a
-// multiple of 16).
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // Barrier over the 128 threads of consumer group `id` that also ANDs `v`
 // across them: every decision taken after it is the same on the whole group.
 __device__ __forceinline__ bool group_and(bool v, int id) {

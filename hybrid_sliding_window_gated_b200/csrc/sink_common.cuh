@@ -53,10 +53,6 @@ __device__ __forceinline__ float bf16_f32(uint16_t v) {
 __device__ __forceinline__ int pair_lo(int j, int P) { return j < P ? j : 2 * j; }
 __device__ __forceinline__ int pair_hi(int j, int P) { return j < P ? j + P : 2 * j + 1; }
 
-__device__ __forceinline__ float2 cmul(float2 x, float2 y) {
-  return make_float2(x.x * y.x - x.y * y.y, x.x * y.y + x.y * y.x);
-}
-
 // Byte offset of 16-byte chunk c of row r of a K', V, q' or dA tile: eight rows
 // at one chunk index lie in eight different 16-byte bank groups.
 __device__ __forceinline__ uint32_t row_off(int r, int c) {

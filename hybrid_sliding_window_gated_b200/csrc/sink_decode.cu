@@ -94,15 +94,6 @@ __device__ __forceinline__ uint32_t tile_off(int s, int c, int half) {
   return static_cast<uint32_t>((c >> 3) * half + s * 128 + (((c & 7) ^ (s & 7)) << 4));
 }
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // Barrier over a group's 160 threads that also ANDs v across them.
 __device__ __forceinline__ bool group_and(bool v, int id) {
   uint32_t r;
@@ -509,7 +500,8 @@ int launch_sink_decode(const CUtensorMap& tk, const CUtensorMap& tv, const CUten
   const int fixed =
       static_cast<int>(sizeof(snd::Control)) + snd::kGroups * snd::qa_bytes(a.G) + 1024;
   a.stage_bytes = snd::stage_size(a.s8, a.G);
-  // Three units in flight where they fit (up to 8 sinks, or 16 with few heads), else two.
+  // Three units in flight where they fit (no sinks, or up to 8 and at most four heads per KV
+  // head), else two.
   a.stages = 3 * a.stage_bytes + fixed <= kLimit ? 3 : 2;
   static std::atomic<int> configured[64];
   if (!configured[di.device].load(std::memory_order_acquire)) {
