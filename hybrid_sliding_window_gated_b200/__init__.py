@@ -148,10 +148,15 @@ def _new(stream, make, *args, device, shared=True, **kw):
     return t
 
 
+def _like(stream, x):
+    return torch.empty_like(x) if stream is None else _new(stream, torch.empty_like, x,
+                                                           device=x.device)
+
+
 def _grads(stream, q, k, v, g):
     """What a backward writes (dq, dk, dv, dg) and adds into (dwq, dwk, from zero)."""
     D, device = q.shape[-1], q.device
-    return (*(_new(stream, torch.empty_like, t, device=device) for t in (q, k, v, g)),
+    return (*(_like(stream, t) for t in (q, k, v, g)),
             *(_new(stream, torch.zeros, D, dtype=torch.float32, device=device) for _ in range(2)))
 
 
@@ -200,11 +205,10 @@ def _need(where, device, **tensors):
                              f"the device of the first input")
 
 
-def _alike(where, **caches):
+def _alike(where, name, k, v):
     """A K cache's sizes lay out the V cache too: one of another capacity would be misread."""
-    (nk, k), (nv, v) = caches.items()
     if k.numel() != v.numel():
-        raise ValueError(f"{where}: {nk} has {k.numel()} elements, {nv} {v.numel()}")
+        raise ValueError(f"{where}: k_{name} has {k.numel()} elements, v_{name} {v.numel()}")
 
 
 def _on_current_device(where, device):
@@ -229,7 +233,7 @@ def fwd(q, k, v, g, wq, wk, *, window=128, rot_dim=42, rope_base=1e4, eps=1e-6, 
     B, T, Hq, D = q.shape
     Hkv = k.shape[2]
     if out is None:
-        out = _new(stream, torch.empty_like, q, device=q.device)
+        out = _like(stream, q)
     if want_lse and lse is None:
         lse = _new(stream, torch.empty, (B, Hq, T), dtype=torch.float32, device=q.device)
     p = make_params(B, T, Hq, Hkv, head_dim=D, window=window, rot_dim=rot_dim,
@@ -252,7 +256,7 @@ def fwd_halo(q, k, v, g, wq, wk, k_halo, v_halo, pos0, *, window=128, rot_dim=42
     B, T, Hq, D = q.shape
     Hkv = k.shape[2]
     if out is None:
-        out = _new(stream, torch.empty_like, q, device=q.device)
+        out = _like(stream, q)
     if want_lse and lse is None:
         lse = _new(stream, torch.empty, (B, Hq, T), dtype=torch.float32, device=q.device)
     p = make_params(B, T, Hq, Hkv, head_dim=D, window=window, rot_dim=rot_dim,
@@ -431,7 +435,7 @@ def decode_step(pos, q, k_new, v_new, g, wq, wk, k_cache, v_cache, *, rot_dim=42
     N, Hq, D = q.shape
     Hkv, W = k_cache.shape[1], k_cache.shape[2]
     if out is None:
-        out = _new(stream, torch.empty_like, q, device=q.device)
+        out = _like(stream, q)
     p = make_params(N, 1, Hq, Hkv, head_dim=D, window=W, rot_dim=rot_dim, rope_base=rope_base,
                     eps=eps, scale=scale, flags=flags)
     nq, nk = N * Hq * D, N * Hkv * D
@@ -476,7 +480,7 @@ def global_fwd(q, k, v, wq, wk, k_cache, v_cache, *, rot_dim=42, rope_base=1e4, 
     Hkv = k.shape[2]
     cap = k_cache.shape[2]
     if out is None:
-        out = _new(stream, torch.empty_like, q, device=q.device)
+        out = _like(stream, q)
     if want_lse and lse is None:
         lse = _new(stream, torch.empty, (B, Hq, T), dtype=torch.float32, device=q.device)
     p = make_params(B, T, Hq, Hkv, head_dim=D, window=0, rot_dim=rot_dim, rope_base=rope_base,
@@ -508,7 +512,7 @@ def global_decode_step(pos, q, k_new, v_new, wq, wk, k_cache, v_cache, *, rot_di
     N, Hq, D = q.shape
     Hkv, cap = k_cache.shape[1], k_cache.shape[2]
     if out is None:
-        out = _new(stream, torch.empty_like, q, device=q.device)
+        out = _like(stream, q)
     p = make_params(N, 1, Hq, Hkv, head_dim=D, window=0, rot_dim=rot_dim, rope_base=rope_base,
                     eps=eps, scale=scale, flags=flags)
     nbytes = int(lib().swa_global_decode_workspace_size(ctypes.byref(p), cap))
@@ -560,7 +564,7 @@ def sink_fwd(q, k, v, g, wq, wk, n_sink, *, window=128, rot_dim=42, rope_base=1e
     B, T, Hq, D = q.shape
     Hkv = k.shape[2]
     if out is None:
-        out = _new(stream, torch.empty_like, q, device=q.device)
+        out = _like(stream, q)
     if want_lse and lse is None:
         lse = _new(stream, torch.empty, (B, Hq, T), dtype=torch.float32, device=q.device)
     p = make_params(B, T, Hq, Hkv, head_dim=D, window=window, rot_dim=rot_dim,
@@ -615,7 +619,7 @@ def sink_decode_step(pos, q, k_new, v_new, g, wq, wk, k_cache, v_cache, k_sink, 
     Hkv, W = k_cache.shape[1], k_cache.shape[2]
     S = 0 if k_sink is None else k_sink.shape[2]
     if out is None:
-        out = _new(stream, torch.empty_like, q, device=q.device)
+        out = _like(stream, q)
     p = make_params(N, 1, Hq, Hkv, head_dim=D, window=W, rot_dim=rot_dim, rope_base=rope_base,
                     eps=eps, scale=scale, flags=flags)
     nq, nk = N * Hq * D, N * Hkv * D
@@ -626,9 +630,9 @@ def sink_decode_step(pos, q, k_new, v_new, g, wq, wk, k_cache, v_cache, k_sink, 
           k_new=(k_new, bf, nk), v_new=(v_new, bf, nk), g=(g, bf, nq),
           wq=(wq, f32, D if N else 0), wk=(wk, f32, D if N else 0),
           k_cache=(k_cache, bf, nk * W), v_cache=(v_cache, bf, nk * W), out=(out, bf, nq), **sinks)
-    _alike("swa_sink_decode_step", k_cache=k_cache, v_cache=v_cache)
+    _alike("swa_sink_decode_step", "cache", k_cache, v_cache)
     if sinks:
-        _alike("swa_sink_decode_step", k_sink=k_sink, v_sink=v_sink)
+        _alike("swa_sink_decode_step", "sink", k_sink, v_sink)
     rc = lib().swa_sink_decode_step(ctypes.byref(p), S, _ptr(pos), _ptr(q), _ptr(k_new),
                                     _ptr(v_new), _ptr(g), _ptr(wq), _ptr(wk), _ptr(k_cache),
                                     _ptr(v_cache), _ptr(k_sink), _ptr(v_sink), _ptr(out),
@@ -653,7 +657,7 @@ def prefill_to_sinks(k, v, wk, k_sink, v_sink, starts=None, lens=None, pos0=None
     _need("swa_prefill_to_sinks", k_sink.device, k=(k, bf, nk), v=(v, bf, nk),
           wk=(wk, torch.float32, D if n else 0), k_sink=(k_sink, bf, n), v_sink=(v_sink, bf, n),
           **extra)
-    _alike("swa_prefill_to_sinks", k_sink=k_sink, v_sink=v_sink)
+    _alike("swa_prefill_to_sinks", "sink", k_sink, v_sink)
     rc = lib().swa_prefill_to_sinks(ctypes.byref(p), S, _ptr(starts), _ptr(lens), _ptr(pos0),
                                     _ptr(k), _ptr(v), _ptr(wk), _ptr(k_sink), _ptr(v_sink),
                                     _stream(stream))
@@ -682,7 +686,7 @@ def global_decode_shared(pos, q, k_new, v_new, wq, wk, k_prefix, v_prefix, prefi
                          f"k_cache {Hkv}")
     pcap = k_prefix.shape[-2]
     if out is None:
-        out = _new(stream, torch.empty_like, q, device=q.device)
+        out = _like(stream, q)
     p = make_params(N, 1, Hq, Hkv, head_dim=D, window=0, rot_dim=rot_dim, rope_base=rope_base,
                     eps=eps, scale=scale, flags=flags)
     nbytes = int(lib().swa_global_decode_shared_workspace_size(ctypes.byref(p), prefix_len, cap))
@@ -696,8 +700,8 @@ def global_decode_shared(pos, q, k_new, v_new, wq, wk, k_prefix, v_prefix, prefi
           wk=(wk, f32, D if N else 0), k_prefix=(k_prefix, bf, npre), v_prefix=(v_prefix, bf, npre),
           k_cache=(k_cache, bf, nk * cap), v_cache=(v_cache, bf, nk * cap), out=(out, bf, nq),
           workspace=(workspace, torch.uint8, nbytes if N else 0))
-    _alike("swa_global_decode_shared", k_prefix=k_prefix, v_prefix=v_prefix)
-    _alike("swa_global_decode_shared", k_cache=k_cache, v_cache=v_cache)
+    _alike("swa_global_decode_shared", "prefix", k_prefix, v_prefix)
+    _alike("swa_global_decode_shared", "cache", k_cache, v_cache)
     rc = lib().swa_global_decode_shared(ctypes.byref(p), prefix_len, pcap, _ptr(k_prefix),
                                         _ptr(v_prefix), _ptr(pos), _ptr(q), _ptr(k_new),
                                         _ptr(v_new), _ptr(wq), _ptr(wk), _ptr(k_cache),
