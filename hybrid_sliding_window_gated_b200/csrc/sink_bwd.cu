@@ -280,10 +280,11 @@ __global__ void __launch_bounds__(256, 4) sink_bwd_rows_kernel(const SinkBwdArgs
         l2[e] = NAN;
       }
     }
+    // the two rows' sums, row 0's in lanes below 16 and row 1's above
+    const bool up = lane & 16;
+    float Ds = (up ? D[1] : D[0]) + __shfl_xor_sync(0xffffffffu, up ? D[0] : D[1], 16);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-      for (int e = 0; e < kN; ++e) D[e] += __shfl_xor_sync(0xffffffffu, D[e], o);
+    for (int o = 8; o > 0; o >>= 1) Ds += __shfl_xor_sync(0xffffffffu, Ds, o);
     // the stage holds rows i & 7 .. of an eight-row tile
     uint8_t* qt = stage[warp][0] - (i & 7) * kRowBytes;
     uint8_t* dt = stage[warp][1] - (i & 7) * kRowBytes;
@@ -298,8 +299,8 @@ __global__ void __launch_bounds__(256, 4) sink_bwd_rows_kernel(const SinkBwdArgs
           pack_f16x2(u0[e].x * f, u0[e].y * f);
       *reinterpret_cast<uint32_t*>(dt + row_off(r, 4 * md + q + 1) + 4 * c) =
           pack_f16x2(u1[e].x * f, u1[e].y * f);
-      if (lane == 0)
-        a.row[out + i + e] = make_float4(l2[e], be, fabsf(D[e]) < INFINITY ? D[e] : 0.f, 0.f);
+      if (lane == 16 * e)
+        a.row[out + i + e] = make_float4(l2[e], be, fabsf(Ds) < INFINITY ? Ds : 0.f, 0.f);
     }
     if (i + kN < 16) fetch_row(i + kN);
     __syncwarp();
@@ -599,10 +600,10 @@ __global__ void __launch_bounds__(kQThreads, 2) sink_bwd_q_kernel(const SinkBwdA
       asm volatile("prefetch.global.L2 [%0];" ::"l"(
           a.q + ((static_cast<long long>(b) * a.T + t) * a.Hq + hq) * kHeadDim + 64 * (lane & 1)));
     }
-    // ---- S and dP of all blocks; P and dP - mid stay in registers (fp16) until D, the
-    // sum of P dP, is known.  mid is D from the forward's o, as exact as its rounding
-    // allows: where a row's probability sits on few keys their dP is near D, and dP itself
-    // in fp16 would leave 2^-11 of it in the difference.
+    // ---- S and dP of all blocks; P and dP - mid stay in registers (fp16) until D - mid, the
+    // sum of their products, is known.  mid is D from the forward's o, as exact as its
+    // rounding allows: where a row's probability sits on few keys their dP is near D, and dP
+    // itself in fp16 would leave 2^-11 of it in the difference.
     uint32_t pf[10][4], gf[10][4];
     Dn[0] = Dn[1] = 0.f;
 #pragma unroll
@@ -639,7 +640,7 @@ __global__ void __launch_bounds__(kQThreads, 2) sink_bwd_q_kernel(const SinkBwdA
           for (int e = 0; e < 4; ++e) {
             const int rr = e >> 1, row = r + 8 * rr, col = 8 * n + 2 * c + (e & 1);
             p[e] = ex2_approx(fmaf(s[n][e], sc, -L2[rr]));
-            y[e] = dp[n][e] * ((e & 1) ? f2.y : f2.x);
+            y[e] = fmaf(dp[n][e], (e & 1) ? f2.y : f2.x, -mid[rr]);
             bool hide = false;
             if (x == 0) hide = col <= row;
             if (x == 8) hide = col > row;
@@ -648,8 +649,8 @@ __global__ void __launch_bounds__(kQThreads, 2) sink_bwd_q_kernel(const SinkBwdA
           }
           pf[x][2 * n] = pack_f16x2(p[0], p[1]);
           pf[x][2 * n + 1] = pack_f16x2(p[2], p[3]);
-          gf[x][2 * n] = pack_f16x2(y[0] - mid[0], y[1] - mid[0]);
-          gf[x][2 * n + 1] = pack_f16x2(y[2] - mid[1], y[3] - mid[1]);
+          gf[x][2 * n] = pack_f16x2(y[0], y[1]);
+          gf[x][2 * n + 1] = pack_f16x2(y[2], y[3]);
           Dn[0] += p[0] * y[0] + p[1] * y[1];
           Dn[1] += p[2] * y[2] + p[3] * y[3];
         }
@@ -663,8 +664,7 @@ __global__ void __launch_bounds__(kQThreads, 2) sink_bwd_q_kernel(const SinkBwdA
       Dn[rr] += __shfl_xor_sync(0xffffffffu, Dn[rr], 1);
       Dn[rr] += __shfl_xor_sync(0xffffffffu, Dn[rr], 2);
       if (c == 0)
-        reinterpret_cast<float2*>(a.row + hrow + r + 8 * rr)[1] = make_float2(Dn[rr], am);
-      Dn[rr] -= mid[rr];
+        reinterpret_cast<float2*>(a.row + hrow + r + 8 * rr)[1] = make_float2(Dn[rr] + mid[rr], am);
     }
     // ---- dQ = dS K', dS = P (dP - D)
     float dq[16][4];

@@ -116,15 +116,12 @@ __device__ __forceinline__ void rest_pos(int lane, int* chunk0, int* byte) {
   }
 }
 
-// x, or 0 for what is not a finite fp16 number.  An operand tile holds no such values: a
-// masked pair's 0 x NaN would reach the sums of the rows around it.  Where the pair is
-// visible the row's lse is NaN, and P with it.
-__device__ __forceinline__ float finite(float x) { return fabsf(x) <= 65504.0f ? x : 0.0f; }
-
 // k' / ck of N rows, fp16, in rope order into rows r0 .. of `tile`; w_* are this lane's
 // weights divided by ck, rot its pair's rotation at each row's position.  eps of a row that
-// only fills up a tile is not 0, so that the row's zeros stay zeros.  The rows' chains of
-// shuffles run side by side.
+// only fills up a tile is not 0, so that the row's zeros stay zeros.  A row that has no
+// finite k' (an infinity or NaN, or all zeros with eps = 0) becomes zeros too: a masked
+// pair's 0 x NaN would reach the sums of the rows around it, and where the pair is visible
+// the query's lse is NaN, and P with it.  The rows' chains of shuffles run side by side.
 template <int N>
 __device__ __forceinline__ void store_k_rows(uint8_t* tile, int r0, const KRow (&x)[N], int lane,
                                              float w_lo, float w_hi, float4 w_rest,
@@ -144,13 +141,17 @@ __device__ __forceinline__ void store_k_rows(uint8_t* tile, int r0, const KRow (
   uint32_t pair[N], r01[N], r23[N];
 #pragma unroll
   for (int e = 0; e < N; ++e) {
-    const float rinv = rsqrtf(ss[e] * (1.0f / kHeadDim) + eps[e]);
-    const float u = bf16_f32(x[e].lo) * rinv * w_lo, v = bf16_f32(x[e].hi) * rinv * w_hi;
-    pair[e] = pack_f16x2(finite(u * rot[e].x - v * rot[e].y), finite(v * rot[e].x + u * rot[e].y));
-    r01[e] = pack_f16x2(finite(bf16_lo(x[e].rest.x) * rinv * w_rest.x),
-                        finite(bf16_hi(x[e].rest.x) * rinv * w_rest.y));
-    r23[e] = pack_f16x2(finite(bf16_lo(x[e].rest.y) * rinv * w_rest.z),
-                        finite(bf16_hi(x[e].rest.y) * rinv * w_rest.w));
+    float rinv = rsqrtf(ss[e] * (1.0f / kHeadDim) + eps[e]);
+    KRow y = x[e];
+    if (!(ss[e] < INFINITY && rinv < INFINITY)) {  // the same for the whole warp
+      y.lo = y.hi = 0;
+      y.rest = make_uint2(0u, 0u);
+      rinv = 0.0f;
+    }
+    const float u = bf16_f32(y.lo) * rinv * w_lo, v = bf16_f32(y.hi) * rinv * w_hi;
+    pair[e] = pack_f16x2(u * rot[e].x - v * rot[e].y, v * rot[e].x + u * rot[e].y);
+    r01[e] = pack_f16x2(bf16_lo(y.rest.x) * rinv * w_rest.x, bf16_hi(y.rest.x) * rinv * w_rest.y);
+    r23[e] = pack_f16x2(bf16_lo(y.rest.y) * rinv * w_rest.z, bf16_hi(y.rest.y) * rinv * w_rest.w);
   }
   int c0, by;
   rest_pos(lane, &c0, &by);
