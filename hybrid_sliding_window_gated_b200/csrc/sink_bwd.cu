@@ -76,6 +76,12 @@ __device__ __forceinline__ float scale_exp(float m) {
 __device__ __forceinline__ float key_factor(float am, float e, float up) {
   return e == e ? pow2i(fmaxf(fminf(am - e, 0.0f) - up, -126.0f)) : e;
 }
+// The larger of two numbers; NaN if either is.
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
 // v 2^x for whole x in [-252, 252], in two steps
 __device__ __forceinline__ float scale2(float v, float x) {
   const float h = truncf(0.5f * x);
@@ -270,15 +276,10 @@ __global__ void __launch_bounds__(256, 4) sink_bwd_rows_kernel(const SinkBwdArgs
         *reinterpret_cast<uint2*>(
             a.dg + ((static_cast<long long>(b) * a.T + t) * a.Hq + hq) * kHeadDim + 4 * lane) =
             make_uint2(pack_bf16x2(y0.x, y0.y), pack_bf16x2(y1.x, y1.y));
+      const float mx = max_nan(max_nan(fabsf(u0[e].x), fabsf(u0[e].y)),
+                               max_nan(fabsf(u1[e].x), fabsf(u1[e].y)));
       // magnitudes order as their bits do, NaN above all
-      const uint32_t mx = max(max(__float_as_uint(fabsf(u0[e].x)), __float_as_uint(fabsf(u0[e].y))),
-                              max(__float_as_uint(fabsf(u1[e].x)), __float_as_uint(fabsf(u1[e].y))));
-      m[e] = __uint_as_float(__reduce_max_sync(0xffffffffu, mx));
-      if (!(m[e] < INFINITY)) {  // a row that is not finite: zeros, and an lse of NaN
-        u0[e] = u1[e] = make_float2(0.f, 0.f);
-        m[e] = 0.f;
-        l2[e] = NAN;
-      }
+      m[e] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
     }
     // the two rows' sums, row 0's in lanes below 16 and row 1's above
     const bool up = lane & 16;
@@ -292,15 +293,17 @@ __global__ void __launch_bounds__(256, 4) sink_bwd_rows_kernel(const SinkBwdArgs
     const int md = lane >> 3, c = (lane & 7) >> 1, q = 2 * (lane & 1);
 #pragma unroll
     for (int e = 0; e < kN; ++e) {
-      const float be = scale_exp(m[e]), f = pow2i(be);
+      const bool bad = !(m[e] < INFINITY);  // a row that is not finite: zeros, lse NaN
+      const float be = bad ? kNoScale : scale_exp(m[e]), f = pow2i(be);
       bm = fminf(bm, be);
       const int r = (i & 7) + e;
       *reinterpret_cast<uint32_t*>(dt + row_off(r, 4 * md + q) + 4 * c) =
-          pack_f16x2(u0[e].x * f, u0[e].y * f);
+          bad ? 0u : pack_f16x2(u0[e].x * f, u0[e].y * f);
       *reinterpret_cast<uint32_t*>(dt + row_off(r, 4 * md + q + 1) + 4 * c) =
-          pack_f16x2(u1[e].x * f, u1[e].y * f);
+          bad ? 0u : pack_f16x2(u1[e].x * f, u1[e].y * f);
       if (lane == 16 * e)
-        a.row[out + i + e] = make_float4(l2[e], be, fabsf(Ds) < INFINITY ? Ds : 0.f, 0.f);
+        a.row[out + i + e] =
+            make_float4(bad ? NAN : l2[e], be, fabsf(Ds) < INFINITY ? Ds : 0.f, 0.f);
     }
     if (i + kN < 16) fetch_row(i + kN);
     __syncwarp();

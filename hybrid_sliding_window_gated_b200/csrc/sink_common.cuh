@@ -141,17 +141,15 @@ __device__ __forceinline__ void store_k_rows(uint8_t* tile, int r0, const KRow (
   uint32_t pair[N], r01[N], r23[N];
 #pragma unroll
   for (int e = 0; e < N; ++e) {
-    float rinv = rsqrtf(ss[e] * (1.0f / kHeadDim) + eps[e]);
-    KRow y = x[e];
-    if (!(ss[e] < INFINITY && rinv < INFINITY)) {  // the same for the whole warp
-      y.lo = y.hi = 0;
-      y.rest = make_uint2(0u, 0u);
-      rinv = 0.0f;
-    }
-    const float u = bf16_f32(y.lo) * rinv * w_lo, v = bf16_f32(y.hi) * rinv * w_hi;
+    const float rinv = rsqrtf(ss[e] * (1.0f / kHeadDim) + eps[e]);
+    const float u = bf16_f32(x[e].lo) * rinv * w_lo, v = bf16_f32(x[e].hi) * rinv * w_hi;
     pair[e] = pack_f16x2(u * rot[e].x - v * rot[e].y, v * rot[e].x + u * rot[e].y);
-    r01[e] = pack_f16x2(bf16_lo(y.rest.x) * rinv * w_rest.x, bf16_hi(y.rest.x) * rinv * w_rest.y);
-    r23[e] = pack_f16x2(bf16_lo(y.rest.y) * rinv * w_rest.z, bf16_hi(y.rest.y) * rinv * w_rest.w);
+    r01[e] = pack_f16x2(bf16_lo(x[e].rest.x) * rinv * w_rest.x,
+                        bf16_hi(x[e].rest.x) * rinv * w_rest.y);
+    r23[e] = pack_f16x2(bf16_lo(x[e].rest.y) * rinv * w_rest.z,
+                        bf16_hi(x[e].rest.y) * rinv * w_rest.w);
+    const float f = ss[e] * rinv;  // NaN for inf * 0, 0 * inf and NaN
+    if (f != f) pair[e] = r01[e] = r23[e] = 0u;
   }
   int c0, by;
   rest_pos(lane, &c0, &by);
