@@ -26,7 +26,10 @@
 // Numbers.  The caches are bf16, so the operands of a product are too.  q' enters
 // as two bf16 terms (its value and what the rounding left over: 16 bits of
 // mantissa, half as many products again in all); one term alone adds 1.7e-3
-// relative error to o, which already carries P's and the output's rounding.
+// relative error to o, which already carries P's and the output's rounding.  P enters as
+// one bf16 term (o 2.0 to 2.4e-3 off, 1.7e-3 by its own rounding alone): the own-keys
+// kernel has spare MMA rows for a second, here it would be 8 more MMAs on the 24 per pair
+// of tiles that bound the kernel.
 // S, row sums and O are fp32.  The cache's keys are the caller's, so the softmax
 // assumes no bound on them: each row keeps a reference maximum, and only when a
 // tile exceeds it by 2^8 are the row's O and sum rescaled (P <= 2^8 meanwhile,

@@ -36,9 +36,11 @@
 // of 16 x 16 waste little of the 128-key band (1.1 of 1), where tcgen05's 128 rows
 // of two heads would compute 1.6 times the products and hand S, dP, P and dS through
 // TMEM; the two passes instead of one with atomics cost two products, since a band
-// keeps dK and dV of 192 keys live, too many for registers.
+// keeps dK and dV of 192 keys live, too many for registers.  Neither pass is bound by the
+// products (below), so that count does not speak against tcgen05, on which these two
+// passes were not built: the window backward, built there, takes 770 us at this shape.
 //
-// Measured there (us): kv 41, rows 170, q 350, sinks 62 + 5, k 334, w 6; the
+// Measured there (us): kv 44, rows 192, q 354, sinks 65 + 5, k 336, w 6; the
 // key-major pass reads its operands from shared memory at 66 % of the pipe's rate
 // with the tensor pipe at 44 %, and the query-major pass is its S - P - dS chain.
 //
@@ -179,8 +181,9 @@ __global__ void __launch_bounds__(256) sink_bwd_kv_kernel(const SinkBwdArgs a) {
 // One warp per 16 tokens of a query head, two rows at a time and four dims per lane:
 // q' and dA as operand rows, dg, and the rows' lse and exponent b.  Bound by memory:
 // 1 KiB read and 768 bytes written per row.  The next two rows are on their way to
-// shared memory while a pair is worked on (170 us for 16,384 tokens of 32 heads,
-// 241 with plain loads and as many warps).
+// shared memory while a pair is worked on: 170 us for 16,384 tokens of 32 heads against
+// 241 with plain loads and as many warps, and 192 us with D's estimate and the checks for
+// rows that are not finite (issue slots 81 %, DRAM 59 %).
 __global__ void __launch_bounds__(256, 4) sink_bwd_rows_kernel(const SinkBwdArgs a) {
   constexpr int kN = 2;
   __shared__ __align__(16) uint8_t in[8][2][4][kN * kRowBytes];  // q, g, dO, o as they are

@@ -36,10 +36,11 @@
 // What bounds it: the regions' chain per unit (64 tokens of two heads), about 27,000
 // cycles of which the MMAs are 1,700: Q' 2.4k, K' 3.5k and V 2k of the owner, maximum
 // 2k, P 4.9k, gate and store 7.5k, waits for S and O 3.5k.  4 x 4096 tokens of 32 heads:
-// 230 us, 31 % of the measured copy rate (the plain forward: 143 us, without the
+// 228 us, 31 % of the measured copy rate (the plain forward: 143 us, without the
 // maximum, with 128-token tiles and bf16 operands).  A run starts with its first K tiles
 // loaded straight into the ring and shared by the regions, and the tokens' rotations
-// evaluated once per CTA: 1 x 256 tokens of 4 / 1 heads 28.5 -> 26.3 us.  Measured instead:
+// evaluated once per CTA: 1 x 256 tokens of 4 / 1 heads 28.5 -> 26.3 us cold (24 us back to
+// back).  Measured instead:
 //   - warp MMAs (m16n8k16) on 16 tokens x 2 heads per warp, S, P and O in registers,
 //     eight warps per SM: 320 us (their operands' shared-memory reads and latency);
 //     with 16 warps and one head each, bf16 P and spills: 252 us.

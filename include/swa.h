@@ -329,7 +329,8 @@ int swa_global_decode_step(const swa_params_t* p, const int64_t* pos, const swa_
  * and (i - j < window or j < n_sink); a sink inside the window counts once.
  * Norm, RoPE (at the tokens' own positions), GQA and gate are those of swa_fwd,
  * and n_sink = 0 is swa_fwd's formula.  0 <= n_sink <= 16 (a negative one
- * returns SWA_ERR_INVALID_ARG, more than 16 SWA_ERR_UNSUPPORTED).  No
+ * returns SWA_ERR_INVALID_ARG, more than 16 SWA_ERR_UNSUPPORTED, and so do more
+ * than 2^24 tiles of 64 tokens and one KV head, 256 GB of k).  No
  * counterpart in the pages: a window layer that streams past its window keeps
  * the attention mass that the first tokens draw.
  *
