@@ -419,3 +419,42 @@ def test_backward_of_a_few_tokens(T, seed):
     """dS = P (dP - D) cancels where a row's probability sits on few keys: the difference,
     not dP, is what fp16 rounds, so the bar of every other shape holds here."""
     check_backward(su.draw(1, T, 2, 1, seed=seed, grad=True), 4)
+
+
+# --------------------------------------------- streams that are not torch's
+
+
+class RawStream:
+    def __init__(self, pointer):
+        self.cuda_stream = pointer
+
+
+@pytest.mark.parametrize("name", ["sink_bwd", "global_decode_shared", "fwd"])
+def test_streams_of_other_libraries(name):
+    """An object with a raw stream pointer, the legacy default stream among them."""
+    call = calls()[name]
+    want = [y.clone() for y in outputs(call(None))]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for pointer in (s.cuda_stream, 0):
+        got = outputs(call(RawStream(pointer)))
+        torch.cuda.synchronize()
+        same(name, got, want)
+    ok()
+
+
+def test_stream_argument_in_a_captured_graph():
+    t, dO = training(seed=210)
+    o, lse = swa.sink_fwd(*t, 4, want_lse=True)
+    want = swa.sink_bwd(*t, o, lse, dO, 4)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        o2, l2 = swa.sink_fwd(*t, 4, want_lse=True, stream=s)
+        got = swa.sink_bwd(*t, o2, l2, dO, 4, stream=s)
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o2, o) and all(torch.equal(a, b) for a, b in zip(got, want))
+    ok()
