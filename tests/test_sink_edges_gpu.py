@@ -280,7 +280,7 @@ def test_forward_keeps_small_dims_of_v(top):
 def gathered_forward(q, k, v, g, wq, wk, n_sink, R=42, base=1e4):
     """su.sink_forward for one sequence, each query's keys gathered at once (64 bits)."""
     T, Hq, Hkv = q.shape[1], q.shape[2], k.shape[2]
-    dev = q.device
+    dev, n_sink = q.device, min(n_sink, q.shape[1])
     cpu = lambda y, w: su.norm_rope(y.cpu(), w.cpu(), torch.arange(T).expand(1, T), R, base).to(dev)
     qq, kk = cpu(q, wq)[0].reshape(T, Hkv, -1, 128), cpu(k, wk)[0]
     i = torch.arange(T, device=dev)
