@@ -30,13 +30,16 @@
 // the 64-bit value, of which bf16's rounding of o alone is 1.66e-3.
 //
 // Values that are not finite.  A masked key has P = 0, but 0 * inf and 0 * NaN are NaN
-// in a product of tiles: a row whose O is not finite is summed again key by key,
-// without the keys of P = 0.
+// in a product of tiles: a V row that is not finite enters the tile as zeros and takes no
+// part in the scales of the others, and the queries that see it are summed again key by
+// key.  A K row that is not finite makes P of those that see it NaN.  Sequences of 4096
+// whose last 100 tokens are NaN cost 252 us below (940 when rows were summed again wherever
+// O was not finite).
 //
 // What bounds it: the regions' chain per unit (64 tokens of two heads), about 27,000
 // cycles of which the MMAs are 1,700: Q' 2.4k, K' 3.5k and V 2k of the owner, maximum
 // 2k, P 4.9k, gate and store 7.5k, waits for S and O 3.5k.  4 x 4096 tokens of 32 heads:
-// 228 us, 31 % of the measured copy rate (the plain forward: 143 us, without the
+// 220 us, 33 % of the measured copy rate (the plain forward: 143 us, without the
 // maximum, with 128-token tiles and bf16 operands).  A run starts with its first K tiles
 // loaded straight into the ring and shared by the regions, and the tokens' rotations
 // evaluated once per CTA: 1 x 256 tokens of 4 / 1 heads 28.5 -> 26.3 us cold (24 us back to
@@ -274,8 +277,8 @@ __device__ __forceinline__ void k_row_pair(const uint8_t* s0, const uint8_t* s1,
   }
 }
 
-// Half a V row from bf16 to fp16 in place; returns the row's exponent a.  `keep`
-// false stores zeros (a sink row past n_sink).
+// Half a V row from bf16 to fp16 in place; returns the row's exponent a.  A row that is
+// not finite becomes zeros, and so does one that `keep` refuses (a sink past n_sink).
 __device__ __forceinline__ float v_half_row(uint8_t* half, int row, bool keep) {
   uint4 x[8];
   uint32_t m = 0;
@@ -288,11 +291,11 @@ __device__ __forceinline__ float v_half_row(uint8_t* half, int row, bool keep) {
   m = max(m & 0xffffu, m >> 16);
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   const float e = keep ? v_exp(__uint_as_float(min(m, 0x7f80u) << 16)) : kZeroRow;
-  const float f = pow2i(e);
+  const float f = pow2i(fmaxf(e, -126.0f));
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     uint4 y = make_uint4(0u, 0u, 0u, 0u);
-    if (keep) {
+    if (keep && e != kBadRow) {
       const float2 s2 = make_float2(f, f);
       const float2 a = __fmul2_rn(unpack2(x[c].x), s2), b = __fmul2_rn(unpack2(x[c].y), s2);
       const float2 d = __fmul2_rn(unpack2(x[c].z), s2), g = __fmul2_rn(unpack2(x[c].w), s2);
@@ -851,6 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int s = 0; s < kSlots; ++s) scaled = scaled || (dist(s) >= 0 && sm.scaled[s] != 0);
       scaled = __any_sync(0xffffffffu, scaled);  // TMEM loads below: one way for the warp
       float am = kVExp;
+      bool sees_bad = false;
       if (scaled) {
         am = 126.0f;
 #pragma unroll 1
@@ -863,12 +867,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float ev[4] = {e.x, e.y, e.z, e.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (d == 0 ? j + i <= tok : (d == 1 || j + i > tok)) am = fminf(am, ev[i]);
+              if (d == 0 ? j + i <= tok : (d == 1 || j + i > tok)) {
+                sees_bad = sees_bad || ev[i] == kBadRow;
+                am = fminf(am, ev[i] == kBadRow ? am : ev[i]);
+              }
           }
         }
         if (see_sinks)
           for (int i = 0; i < kMaxSink; ++i)
-            if (i <= sink_hi) am = fminf(am, sm.va[kSlots * kTok + i]);
+            if (i <= sink_hi) {
+              const float ev = sm.va[kSlots * kTok + i];
+              sees_bad = sees_bad || ev == kBadRow;
+              am = fminf(am, ev == kBadRow ? am : ev);
+            }
         __syncwarp();
       }
       // P = 2^(s sc - ms) as fp16 over the region's first columns, slot by slot: P of
@@ -960,66 +971,69 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float split = am > 64.0f ? 64.0f : 0.0f;
       const float il = 1.0f / l * pow2i(split - am);
       const bool in_two = __any_sync(0xffffffffu, split != 0.0f);  // one way for the warp
+      // (a row sum of NaN makes O NaN by itself)
+      const bool again = __any_sync(0xffffffffu, sees_bad && l == l);
+      const float ilc = again ? 1.0f : il;
 #pragma unroll 1
       for (int ch = 0; ch < kHeadDim / 32; ++ch) {
         uint32_t ov[32];
         tmem_ld32(t_row + 128 + ch * 32, ov);
         tmem_wait_ld();
-        {
-          float2 z = make_float2(0.f, 0.f);
+        if (again) {
+          // These dims again, key by key, from the P in TMEM and V in memory, with the
+          // row's factor on P: beside an infinity V may hold any number.
+          float o[32];
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            z = __ffma2_rn(make_float2(__uint_as_float(ov[2 * i]), __uint_as_float(ov[2 * i + 1])),
-                           make_float2(0.f, 0.f), z);
-          const bool bad = !(z.x + z.y == 0.0f);
-          if (__any_sync(0xffffffffu, bad)) {
-            // These dims again, key by key, from the P in TMEM and V in memory.
-            float o[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+          for (int i = 0; i < 32; ++i) o[i] = 0.f;
 #pragma unroll 1
-            for (int x = 0; x < kRing / 16; ++x) {  // 16 keys: 8 columns of P
-              const int s = x >> 2, d = s < kSlots ? dist(s) : (see_sinks ? 0 : -1);
-              if (d < 0) continue;
-              const int key0 = s < kSlots ? (c.t - d) * kTok + 16 * (x & 3) : 0;
-              uint32_t pw[8];
-              tmem_ld8(t_row + 8 * x, pw);
-              tmem_wait_ld();
+          for (int x = 0; x < kRing / 16; ++x) {  // 16 keys: 8 columns of P
+            const int s = x >> 2, d = s < kSlots ? dist(s) : (see_sinks ? 0 : -1);
+            if (d < 0) continue;
+            const int key0 = s < kSlots ? (c.t - d) * kTok + 16 * (x & 3) : 0;
+            uint32_t pw[8];
+            tmem_ld8(t_row + 8 * x, pw);
+            tmem_wait_ld();
 #pragma unroll 1
-              for (int e = 0; e < 16; ++e) {
-                uint32_t word = pw[0];
+            for (int e = 0; e < 16; ++e) {
+              uint32_t word = pw[0];
 #pragma unroll
-                for (int k = 1; k < 8; ++k) word = (e >> 1) == k ? pw[k] : word;
-                const float2 p2 = __half22float2(*reinterpret_cast<const __half2*>(&word));
-                float p = (e & 1) ? p2.y : p2.x;
-                if (p == 0.0f || key0 + e >= a.T) continue;
-                const uint16_t* vrow =
-                    a.v + ((static_cast<long long>(c.b) * a.T + key0 + e) * a.Hkv + c.kvh) * kHeadDim;
-                float f = pow2i(kVExp);
-                if (scaled) {  // the key's own a (the ring's record may have moved on)
-                  uint32_t m = 0;
-                  for (int i = 0; i < kHeadDim; ++i) m = max(m, vrow[i] & 0x7fffu);
-                  f = pow2i(v_exp(__uint_as_float(min(m, 0x7f80u) << 16)));
-                }
-                const uint4* vr4 = reinterpret_cast<const uint4*>(vrow + 32 * ch);
+              for (int k = 1; k < 8; ++k) word = (e >> 1) == k ? pw[k] : word;
+              const float2 p2 = __half22float2(*reinterpret_cast<const __half2*>(&word));
+              const float p = (e & 1) ? p2.y : p2.x;
+              if (p == 0.0f || key0 + e >= a.T) continue;
+              const uint16_t* vrow =
+                  a.v + ((static_cast<long long>(c.b) * a.T + key0 + e) * a.Hkv + c.kvh) * kHeadDim;
+              // the key's own a (the ring's record may have moved on); a bad row's P was not
+              // scaled
+              uint32_t m = 0;
+#pragma unroll 4
+              for (int i = 0; i < kHeadDim / 8; ++i) {
+                const uint4 w4 = __ldg(reinterpret_cast<const uint4*>(vrow) + i);
+                m = __vmaxu2(m, __vmaxu2(__vmaxu2(w4.x & 0x7fff7fffu, w4.y & 0x7fff7fffu),
+                                         __vmaxu2(w4.z & 0x7fff7fffu, w4.w & 0x7fff7fffu)));
+              }
+              m = max(m & 0xffffu, m >> 16);
+              const float ek = v_exp(__uint_as_float(min(m, 0x7f80u) << 16));
+              const float f = pow2i(ek == kBadRow ? am : ek);
+              const float wt = p * il * f * pow2i(-split);
+              const uint4* vr4 = reinterpret_cast<const uint4*>(vrow + 32 * ch);
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                  const uint4 w4 = __ldg(vr4 + y);
-                  const uint32_t ww[4] = {w4.x, w4.y, w4.z, w4.w};
+              for (int y = 0; y < 4; ++y) {
+                const uint4 w4 = __ldg(vr4 + y);
+                const uint32_t ww[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-                  for (int q = 0; q < 4; ++q) {
-                    o[8 * y + 2 * q] = fmaf(p, f * bf16_lo(ww[q]), o[8 * y + 2 * q]);
-                    o[8 * y + 2 * q + 1] = fmaf(p, f * bf16_hi(ww[q]), o[8 * y + 2 * q + 1]);
-                  }
+                for (int q = 0; q < 4; ++q) {
+                  o[8 * y + 2 * q] = fmaf(wt, bf16_lo(ww[q]), o[8 * y + 2 * q]);
+                  o[8 * y + 2 * q + 1] = fmaf(wt, bf16_hi(ww[q]), o[8 * y + 2 * q + 1]);
                 }
               }
-              __syncwarp();
             }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(o[i]);
+            __syncwarp();
           }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(o[i]);
         }
-        if (in_two) {
+        if (in_two && !again) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             ov[i] = __float_as_uint(__uint_as_float(ov[i]) * pow2i(-split));
@@ -1028,7 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
           mbar_arrive(&sm.tfree[r]);  // the region may take the next Q K^T
         }
-        const float2 il2 = make_float2(il, il);
+        const float2 il2 = make_float2(ilc, ilc);
         uint8_t* half = sm.q[qs] + (ch >> 1) * kQHalf;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

@@ -338,9 +338,11 @@ int swa_global_decode_step(const swa_params_t* p, const int64_t* pos, const swa_
  * see never reaches its output, whatever it holds (NaN and infinities
  * included), so rows behind a padded sequence may hold anything.  q', k' and v enter
  * in fp16 (swa_fwd's in bf16), v under a power-of-two scale of each row: an entry at
- * least 2^-19 of its row's largest keeps all its bf16 bits, a smaller one may lose some.
+ * least 2^-19 of its row's largest keeps all its bf16 bits, a smaller one may lose some,
+ * and so may a key's term below 2^-28 of the largest row of v that its query sees.
  * Tiles with a row of v whose largest entry is not in [2^-6, 128) take longer (4 x 4096
- * tokens of 32 / 8 heads: 384 us where all are such, 225 otherwise).
+ * tokens of 32 / 8 heads: 399 us where all are such, 220 otherwise), and queries that see
+ * a row which is not finite much longer.
  */
 int swa_sink_fwd(const swa_params_t* p, int32_t n_sink, const swa_bf16_t* q, const swa_bf16_t* k,
                  const swa_bf16_t* v, const swa_bf16_t* g, const float* wq, const float* wk,

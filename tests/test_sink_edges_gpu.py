@@ -274,6 +274,27 @@ def test_forward_keeps_small_dims_of_v(top):
     assert d.max() <= REL, d.max()
 
 
+@pytest.mark.parametrize("big", [1.0, 1e32, 1e36, 2e38])
+@pytest.mark.parametrize("around", [1.0, 1e-30, 1e10])
+def test_forward_finite_dims_beside_an_infinity(big, around):
+    """A visible V row with one infinite entry and others of any size: the other dims of the
+    rows that see it come out as the 64-bit form's."""
+    x = su.draw(1, 300, 2, 1, seed=142)
+    x["v"] = (x["v"].float() * around).to(torch.bfloat16)
+    x["v"][0, 100, 0, 5] = float("inf")
+    x["v"][0, 100, 0, 8:24] = big
+    o, _ = forward(x, 4)
+    ok()
+    o_ref, _ = su.sink_forward(*su.args(x, dtype=torch.float64), 4, 42, 1e4)
+    dims = [d for d in range(128) if d != 5]
+    got, want = o.double().cpu()[0, 100:228], o_ref[0, 100:228]
+    assert not torch.isfinite(got[..., 5]).any()
+    assert torch.isfinite(got[..., dims]).all()
+    for part in (range(8, 24), [d for d in dims if not 8 <= d < 24]):
+        d = (got - want)[..., part].norm(dim=-1)
+        assert (d <= 2 * REL * want[..., part].norm(dim=-1)).all()
+
+
 # ----------------------------------------- the backward's other launch shapes
 
 
